@@ -1,0 +1,113 @@
+// kivi_paged.cuh -- what the kernels of the paged cache share: argument
+// blocks, the state of a sequence as it follows from its token count, and the
+// checks of everything that only the device can see (include/kivi.h, "paged
+// cache").
+#pragma once
+
+#include "kivi_internal.cuh"
+
+namespace kivi {
+
+struct PagedArgs {
+    uint8_t *pool;
+    __half *k_fp16, *v_fp16;          // [P][rows][D]
+    int32_t *table;                   // [P][columns]
+    int32_t *n_tokens, *n_evicted;    // [B]
+    unsigned *control;                // status word, then a counter per sequence
+    int64_t num_pages;
+    int columns;
+    int rec_bytes;
+    int bits, fmt, meta, G, flush_group;
+    int R, Ns, rows;
+    int B, Hkv, g;                    // g = query heads per kv head
+    float fp8_k_scale, fp8_v_scale;
+};
+
+struct ChunkArgs {
+    const __half *q, *k, *v;
+    const int32_t *offsets;           // [B + 1]
+    int64_t q_stride, kv_stride;      // halves from token to token
+    int64_t num_tokens;
+    int max_new;
+    float scale_log2;                 // softmax scale * log2(e)
+    float cap_log2, cap_inv;          // cap * log2(e) and scale / cap; cap_log2 = 0: no cap
+    int full;                         // every new token sees all of its sequence's
+    int v8;                           // k, v rows and the fp16 rows 32-byte aligned
+};
+
+// Sequence b as its token count says.
+struct PagedState {
+    int n;            // tokens seen
+    int sink;         // of them in the sink rows
+    int flushed;      // key groups quantised so far (held and evicted)
+    int held;         // pages held: table columns 0 .. held - 1
+    int window;       // tokens in the ring
+    int head;         // slot of the oldest of them
+};
+
+__device__ __forceinline__ int flushed_groups(const PagedArgs &c, int n)
+{
+    const int m = n - c.Ns;
+    if (c.flush_group)
+        return m > c.R ? (m - c.R + c.G - 1) / c.G : 0;
+    return m > 0 ? (m - 1) / c.R * (c.R / c.G) : 0;
+}
+
+// False when the lengths do not fit the table.
+__device__ __forceinline__ bool paged_state(const PagedArgs &c, int b, PagedState &s)
+{
+    s.n = c.n_tokens[b];
+    const int gone = c.n_evicted[b];
+    if (s.n < 0 || gone < 0)
+        return false;
+    s.sink = min(s.n, c.Ns);
+    s.flushed = flushed_groups(c, s.n);
+    s.held = s.flushed - gone;
+    s.window = s.n - s.sink - s.flushed * c.G;
+    s.head = (int)((int64_t)s.flushed * c.G % c.R);
+    return s.held >= 0 && s.held <= c.columns;
+}
+
+// New tokens first .. first + T - 1 of sequence b; false when the offsets are
+// not what the header asks for.
+__device__ __forceinline__ bool chunk_of(const ChunkArgs &x, int b, int &first, int &T)
+{
+    const int lo = x.offsets[b], hi = x.offsets[b + 1];
+    if (lo < 0 || hi < lo || hi > x.num_tokens || hi - lo > x.max_new)
+        return false;
+    first = lo;
+    T = hi - lo;
+    return true;
+}
+
+// Record in column `col` of pair p, or null when the page number is not one of
+// the pool's.
+__device__ __forceinline__ unsigned char *page_record(const PagedArgs &c, int p, int col)
+{
+    const int id = c.table[(int64_t)p * c.columns + col];
+    if (id < 0 || id >= c.num_pages)
+        return nullptr;
+    return c.pool + (int64_t)id * c.rec_bytes;
+}
+
+cudaError_t launch_paged_append(const PagedArgs &c, const ChunkArgs &x, cudaStream_t s, int *launches);
+
+// Work split of an attention or a weights call, and where its parts lie in the
+// workspace: fixed by the sizes alone.
+struct AttendPlan {
+    int splits;           // parts of a pair's tokens
+    int row_tiles;        // tiles of query rows of the longest chunk
+    size_t bytes;         // workspace bytes
+};
+AttendPlan attend_plan(const PagedArgs &c, int max_new, int max_cached);
+AttendPlan weights_plan(const PagedArgs &c, int max_new, int max_cached);
+size_t evict_bytes(const PagedArgs &c);
+
+cudaError_t launch_paged_attention(const PagedArgs &c, const ChunkArgs &x, int max_cached, __half *out,
+                                   void *ws, cudaStream_t s, int *launches);
+cudaError_t launch_paged_weights(const PagedArgs &c, const ChunkArgs &x, int max_cached, float *weights,
+                                 void *ws, cudaStream_t s, int *launches);
+cudaError_t launch_paged_evict(const PagedArgs &c, float *weights, int budget, int recent, void *ws,
+                               cudaStream_t s, int *launches);
+
+}  // namespace kivi

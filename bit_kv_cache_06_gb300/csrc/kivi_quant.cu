@@ -20,7 +20,9 @@
 // channels, then across the G/16 lanes of the group with shuffles.  Values
 // are encoded between the two block barriers.  Traffic per token: 512 B
 // read and 64-128 B written.
-#include "kivi_internal.cuh"
+#include <algorithm>
+
+#include "kivi_paged.cuh"
 
 namespace kivi {
 namespace {
@@ -242,8 +244,11 @@ __device__ __forceinline__ void store_value_codes(unsigned char *row, const uint
     }
 }
 
+// One key group of pair p = (b, h): tokens grp G .. grp G + G - 1 of the
+// concatenation, written as the record at `rec`.
 template <int BITS, int G, int MF>
-__global__ void __launch_bounds__(2 * G) quantize_kv_kernel(QuantArgs a)
+__device__ __forceinline__ void quantize_group(const QuantArgs &a, int64_t grp, int p, int b, int h,
+                                               unsigned char *rec)
 {
     constexpr int D = kHeadDim;
     constexpr int W = G / 16;          // warps
@@ -264,10 +269,6 @@ __global__ void __launch_bounds__(2 * G) quantize_kv_kernel(QuantArgs a)
 
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     const int q = lane >> 3, c16 = lane & 7;
-    const int64_t grp = blockIdx.x;
-    const int p = blockIdx.y;
-    const int b = p / a.Hkv;
-    const int h = p % a.Hkv;
     const int t0 = 16 * w + q;                      // the lane's rows: t0 + 4 i
     const int64_t u0 = grp * G + t0;
 
@@ -286,8 +287,6 @@ __global__ void __launch_bounds__(2 * G) quantize_kv_kernel(QuantArgs a)
             load_row16<false>(concat_row(a, a.v_res, a.v_in, p, b, h, u0 + 4 * i) + 16 * c16, vx[i]);
         }
     }
-    unsigned char *rec = a.hist + ((int64_t)p * (a.cap / G) + a.n_quant / G + grp) * RC::BYTES;
-
     // ---- keys: per-channel min/max over the G tokens (fp16, exact) --------
     {
         uint32_t mm[16];
@@ -399,6 +398,16 @@ __global__ void __launch_bounds__(2 * G) quantize_kv_kernel(QuantArgs a)
     }
 }
 
+template <int BITS, int G, int MF>
+__global__ void __launch_bounds__(2 * G) quantize_kv_kernel(QuantArgs a)
+{
+    const int64_t grp = blockIdx.x;
+    const int p = blockIdx.y;
+    unsigned char *rec =
+        a.hist + ((int64_t)p * (a.cap / G) + a.n_quant / G + grp) * Rec<BITS, G, MF>::BYTES;
+    quantize_group<BITS, G, MF>(a, grp, p, p / a.Hkv, p % a.Hkv, rec);
+}
+
 // ----------------------------------------------------------------- FP8 KV ---
 // "09 -- KV Cache Quantization", "The lazy default: FP8 KV"; "4.4 KV Cache
 // quantization", section 4.2: every element becomes fp8(x / scale) -- x / scale
@@ -433,15 +442,13 @@ __device__ __forceinline__ uint2 fp8_row8(uint4 raw, float s, float r)
 }
 
 template <int FMT>
-__global__ void __launch_bounds__(kThreads) quantize_fp8_kernel(QuantArgs a)
+__device__ __forceinline__ void quantize_fp8_group(const QuantArgs &a, int64_t grp, int p, int b,
+                                                   int h, unsigned char *rec)
 {
-    constexpr int D = kHeadDim, REC = 64 * D;
+    constexpr int D = kHeadDim;
     const int tid = threadIdx.x, c8 = tid % kRowThreads, r = tid / kRowThreads;
-    const int64_t grp = blockIdx.x;
-    const int p = blockIdx.y, b = p / a.Hkv, h = p % a.Hkv;
     const float sk = a.fp8_k_scale, sv = a.fp8_v_scale;
     const float rk = __frcp_rn(sk), rv = __frcp_rn(sv);
-    unsigned char *rec = a.hist + ((int64_t)p * (a.cap / 32) + a.n_quant / 32 + grp) * REC;
 #pragma unroll
     for (int pass = 0; pass < 2; ++pass) {
         const int t = pass * kRowsPerPass + r;                    // token of the record
@@ -451,6 +458,15 @@ __global__ void __launch_bounds__(kThreads) quantize_fp8_kernel(QuantArgs a)
         *reinterpret_cast<uint2 *>(rec + t * D + c8 * 8) = fp8_row8<FMT>(kx, sk, rk);
         *reinterpret_cast<uint2 *>(rec + 32 * D + t * D + c8 * 8) = fp8_row8<FMT>(vx, sv, rv);
     }
+}
+
+template <int FMT>
+__global__ void __launch_bounds__(kThreads) quantize_fp8_kernel(QuantArgs a)
+{
+    const int64_t grp = blockIdx.x;
+    const int p = blockIdx.y;
+    unsigned char *rec = a.hist + ((int64_t)p * (a.cap / 32) + a.n_quant / 32 + grp) * (64 * kHeadDim);
+    quantize_fp8_group<FMT>(a, grp, p, p / a.Hkv, p % a.Hkv, rec);
 }
 
 // 16 tokens x 16 chunks of 16 bytes per CTA: input tokens to fp16 rows (the
@@ -471,6 +487,136 @@ __global__ void __launch_bounds__(kThreads) residual_copy_kernel(ResidArgs a)
     const int64_t dst = ((int64_t)p * a.rows + row) * D + c8 * 8;
     *reinterpret_cast<uint4 *>(a.k_res + dst) = load_stream(a.k_in + src);
     *reinterpret_cast<uint4 *>(a.v_res + dst) = load_stream(a.v_in + src);
+}
+
+// ------------------------------------------------------------ paged append ---
+// The same two steps for a ragged batch whose state is on the device: every
+// block works out from n_tokens and the chunk's offsets what its sequence
+// flushes, quantises group blockIdx.x of it into the page the table names, and
+// leaves at once when there is no such group.
+
+// The concatenation [window, new tokens] of sequence b as QuantArgs, and the
+// groups its append flushes (0 when the sequence is skipped).
+__device__ __forceinline__ int paged_quant_args(const PagedArgs &c, const ChunkArgs &x, int b,
+                                                QuantArgs &a, int &held, unsigned &bad)
+{
+    int first, T;
+    PagedState st;
+    bad = chunk_of(x, b, first, T) ? 0u : KIVI_STATUS_BAD_STATE;
+    if (!bad && !paged_state(c, b, st))
+        bad = KIVI_STATUS_BAD_STATE;
+    if (!bad && (int64_t)st.n + T > 0x7fffffffll)
+        bad = KIVI_STATUS_BAD_STATE;
+    if (bad)
+        return 0;
+    const int due = flushed_groups(c, st.n + T) - st.flushed;
+    held = st.held;
+    if (held + due > c.columns) {
+        bad = KIVI_STATUS_CAPACITY;
+        return 0;
+    }
+    a.k_in = x.k + (int64_t)first * x.kv_stride;
+    a.v_in = x.v + (int64_t)first * x.kv_stride;
+    a.in_sb = 0;
+    a.in_sh = kHeadDim;
+    a.in_st = x.kv_stride;
+    a.skip = min(T, c.Ns - st.sink);
+    a.k_res = c.k_fp16;
+    a.v_res = c.v_fp16;
+    a.rows = c.rows;
+    a.Ns = c.Ns;
+    a.R = c.R;
+    a.head = st.head;
+    a.n_old = st.window;
+    a.fp8_k_scale = c.fp8_k_scale;
+    a.fp8_v_scale = c.fp8_v_scale;
+    a.v8 = x.v8;
+    return due;
+}
+
+// Record of new group grp of pair p, or null when there is none to write.
+__device__ __forceinline__ unsigned char *paged_append_record(const PagedArgs &c, const ChunkArgs &x,
+                                                              int grp, int p, QuantArgs &a)
+{
+    int held = 0;
+    unsigned bad = 0;
+    const int due = paged_quant_args(c, x, p / c.Hkv, a, held, bad);
+    if (grp >= due)
+        return nullptr;
+    unsigned char *rec = page_record(c, p, held + grp);
+    if (!rec && threadIdx.x == 0)
+        atomicOr(c.control, KIVI_STATUS_BAD_PAGE);
+    return rec;
+}
+
+template <int BITS, int G, int MF>
+__global__ void __launch_bounds__(2 * G) paged_quantize_kernel(PagedArgs c, ChunkArgs x)
+{
+    QuantArgs a;
+    const int p = blockIdx.y;
+    unsigned char *rec = paged_append_record(c, x, blockIdx.x, p, a);
+    if (rec)
+        quantize_group<BITS, G, MF>(a, blockIdx.x, p, p / c.Hkv, p % c.Hkv, rec);
+}
+
+template <int FMT>
+__global__ void __launch_bounds__(kThreads) paged_quantize_fp8_kernel(PagedArgs c, ChunkArgs x)
+{
+    QuantArgs a;
+    const int p = blockIdx.y;
+    unsigned char *rec = paged_append_record(c, x, blockIdx.x, p, a);
+    if (rec)
+        quantize_fp8_group<FMT>(a, blockIdx.x, p, p / c.Hkv, p % c.Hkv, rec);
+}
+
+// After the groups are quantised: new tokens that stay fp16 go to their rows
+// (16 rows per block: first the new sink tokens, then those the window keeps),
+// and the last block of a sequence to finish advances n_tokens.  No block
+// waits for another; the last one puts the counter back to zero.
+__global__ void __launch_bounds__(kThreads) paged_rows_kernel(PagedArgs c, ChunkArgs x)
+{
+    constexpr int D = kHeadDim;
+    const int p = blockIdx.y, b = p / c.Hkv, h = p % c.Hkv;
+    QuantArgs a;
+    int held = 0;
+    unsigned bad = 0;
+    const int due = paged_quant_args(c, x, b, a, held, bad);
+    int first = 0, T = 0;
+    if (!bad) {
+        chunk_of(x, b, first, T);
+        const int take = (int)a.skip;
+        const int keep0 = max(due * c.G, a.n_old);            // first kept new token of the concatenation
+        const int kept = a.n_old + (T - take) - keep0;        // may be 0 when all of it is sink
+        const int i = blockIdx.x * kRowsPerPass + threadIdx.x / kRowThreads;
+        const int c8 = threadIdx.x % kRowThreads;
+        if (i < take + kept) {
+            int src, row;
+            if (i < take) {
+                src = i;
+                row = min(c.n_tokens[b], c.Ns) + i;
+            } else {
+                const int u = keep0 + (i - take);
+                src = take + (u - a.n_old);
+                row = c.Ns + (a.head + u) % c.R;
+            }
+            const int64_t from = (int64_t)h * D + (int64_t)src * x.kv_stride + c8 * 8;
+            const int64_t to = ((int64_t)p * c.rows + row) * D + c8 * 8;
+            *reinterpret_cast<uint4 *>(c.k_fp16 + to) = load_stream(a.k_in + from);
+            *reinterpret_cast<uint4 *>(c.v_fp16 + to) = load_stream(a.v_in + from);
+        }
+    } else if (threadIdx.x == 0) {
+        atomicOr(c.control, bad);
+    }
+    __threadfence();
+    __syncthreads();                                          // this block has read n_tokens
+    if (threadIdx.x == 0) {
+        unsigned *ticket = c.control + 1 + b;
+        if (atomicAdd(ticket, 1u) == gridDim.x * (unsigned)c.Hkv - 1u) {
+            *ticket = 0u;
+            if (!bad)
+                c.n_tokens[b] += T;
+        }
+    }
 }
 
 template <int BITS, int MF>
@@ -507,6 +653,40 @@ cudaError_t launch_quantize_fp8(int fmt, const QuantArgs &a, int pairs, cudaStre
         quantize_fp8_kernel<KIVI_FP8_E5M2><<<grid, kThreads, 0, s>>>(a);
     else
         return cudaErrorInvalidValue;
+    return cudaGetLastError();
+}
+
+template <int BITS, int MF>
+static void launch_paged_quantize(const PagedArgs &c, const ChunkArgs &x, dim3 grid, cudaStream_t s)
+{
+    switch (c.G) {
+    case 16: paged_quantize_kernel<BITS, 16, MF><<<grid, 32, 0, s>>>(c, x); break;
+    case 32: paged_quantize_kernel<BITS, 32, MF><<<grid, 64, 0, s>>>(c, x); break;
+    case 64: paged_quantize_kernel<BITS, 64, MF><<<grid, 128, 0, s>>>(c, x); break;
+    default: paged_quantize_kernel<BITS, 128, MF><<<grid, 256, 0, s>>>(c, x); break;
+    }
+}
+
+cudaError_t launch_paged_append(const PagedArgs &c, const ChunkArgs &x, cudaStream_t s, int *launches)
+{
+    const int pairs = c.B * c.Hkv;
+    // a window of R tokens and max_new new ones flush this many groups at most
+    const int groups = (int)std::min<int64_t>(((int64_t)c.R + x.max_new) / c.G, c.columns);
+    const dim3 grid((unsigned)groups, (unsigned)pairs);
+    if (c.fmt == KIVI_FP8_E4M3)
+        paged_quantize_fp8_kernel<KIVI_FP8_E4M3><<<grid, kThreads, 0, s>>>(c, x);
+    else if (c.fmt == KIVI_FP8_E5M2)
+        paged_quantize_fp8_kernel<KIVI_FP8_E5M2><<<grid, kThreads, 0, s>>>(c, x);
+    else if (c.bits == 2)
+        c.meta ? launch_paged_quantize<2, 1>(c, x, grid, s) : launch_paged_quantize<2, 0>(c, x, grid, s);
+    else
+        c.meta ? launch_paged_quantize<4, 1>(c, x, grid, s) : launch_paged_quantize<4, 0>(c, x, grid, s);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess)
+        return e;
+    const int rows = (int)std::min<int64_t>(x.max_new, (int64_t)c.Ns + c.R);
+    paged_rows_kernel<<<dim3((unsigned)((rows + kRowsPerPass - 1) / kRowsPerPass), (unsigned)pairs), kThreads, 0, s>>>(c, x);
+    *launches = 2;
     return cudaGetLastError();
 }
 

@@ -34,6 +34,11 @@ KIVI_FP8_NONE = 0
 KIVI_FP8_E4M3 = 1
 KIVI_FP8_E5M2 = 2
 KIVI_STATUS_WAIT_TIMEOUT = 1
+KIVI_STATUS_BAD_STATE = 2
+KIVI_STATUS_BAD_PAGE = 4
+KIVI_STATUS_CAPACITY = 8
+KIVI_MASK_CAUSAL = 0
+KIVI_MASK_FULL = 1
 
 BUFFER_NAMES = ("history", "k_fp16", "v_fp16")
 BUFFER_DTYPES = (torch.uint8, torch.float16, torch.float16)
@@ -47,6 +52,9 @@ EXPORTED = (
     "kivi_abi_version", "kivi_sizeof_params", "kivi_sizeof_cache",
     "kivi_decode_attention_static", "kivi_decode_static_scratch_bytes",
     "kivi_decode_static_status", "kivi_test_decode_wait_timeout",
+    "kivi_paged_columns", "kivi_paged_control_bytes", "kivi_paged_workspace_bytes",
+    "kivi_paged_init", "kivi_paged_append", "kivi_paged_attention", "kivi_paged_weights",
+    "kivi_paged_evict", "kivi_sizeof_paged", "kivi_sizeof_chunk",
 )
 
 
@@ -76,6 +84,23 @@ class kivi_cache(ctypes.Structure):
                 ("reserved", ctypes.c_int32), ("kernel_launches", ctypes.c_uint64)]
 
 
+class kivi_paged(ctypes.Structure):
+    _fields_ = [("p", kivi_params), ("pool", ctypes.c_void_p), ("k_fp16", ctypes.c_void_p),
+                ("v_fp16", ctypes.c_void_p), ("table", ctypes.c_void_p),
+                ("n_tokens", ctypes.c_void_p), ("n_evicted", ctypes.c_void_p),
+                ("control", ctypes.c_void_p), ("num_pages", ctypes.c_int64),
+                ("kernel_launches", ctypes.c_uint64)]
+
+
+class kivi_chunk(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("offsets", ctypes.c_void_p), ("q_stride", ctypes.c_int64),
+                ("kv_stride", ctypes.c_int64), ("num_tokens", ctypes.c_int64),
+                ("max_new", ctypes.c_int32), ("max_cached", ctypes.c_int32),
+                ("softmax_scale", ctypes.c_float), ("softcap", ctypes.c_float),
+                ("mask", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
 _lib = None
 
 
@@ -89,6 +114,7 @@ def load(path: str = LIB_PATH):
                            "bit_kv_cache_06_gb300.build.build() (needs nvcc)")
     L = ctypes.CDLL(path)
     P, C = ctypes.POINTER(kivi_params), ctypes.POINTER(kivi_cache)
+    PC, X = ctypes.POINTER(kivi_paged), ctypes.POINTER(kivi_chunk)
     vp, i32, i64, sz, f32 = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64,
                              ctypes.c_size_t, ctypes.c_float)
     sigs = {
@@ -114,13 +140,25 @@ def load(path: str = LIB_PATH):
         "kivi_decode_static_scratch_bytes": (sz, []),
         "kivi_decode_static_status": (ctypes.c_int, [vp, vp]),
         "kivi_test_decode_wait_timeout": (ctypes.c_int, [C, vp, vp, vp, sz, vp]),
+        "kivi_paged_columns": (i32, [P]),
+        "kivi_paged_control_bytes": (sz, [P]),
+        "kivi_paged_workspace_bytes": (sz, [P, i32]),
+        "kivi_paged_init": (ctypes.c_int, [PC, P, vp, i64] + [vp] * 6),
+        "kivi_paged_append": (ctypes.c_int, [PC, X, vp]),
+        "kivi_paged_attention": (ctypes.c_int, [PC, X, vp, vp, sz, vp]),
+        "kivi_paged_weights": (ctypes.c_int, [PC, X, vp, vp, sz, vp]),
+        "kivi_paged_evict": (ctypes.c_int, [PC, vp, i32, i32, vp, sz, vp]),
+        "kivi_sizeof_paged": (sz, []),
+        "kivi_sizeof_chunk": (sz, []),
     }
     for name, (res, args) in sigs.items():
         fn = getattr(L, name)
         fn.restype = res
         fn.argtypes = args
     if L.kivi_sizeof_params() != ctypes.sizeof(kivi_params) or \
-            L.kivi_sizeof_cache() != ctypes.sizeof(kivi_cache):
+            L.kivi_sizeof_cache() != ctypes.sizeof(kivi_cache) or \
+            L.kivi_sizeof_paged() != ctypes.sizeof(kivi_paged) or \
+            L.kivi_sizeof_chunk() != ctypes.sizeof(kivi_chunk):
         raise RuntimeError("libkivi struct layout does not match the Python mirror")
     _lib = L
     return L

@@ -360,6 +360,151 @@ double kivi_kv_bytes(int64_t L, int64_t B, int64_t T, int64_t H_kv, int64_t d,
 int kivi_test_decode_wait_timeout(kivi_cache *c, const void *q, void *out,
                                   void *workspace, size_t ws_bytes, kivi_stream_t stream);
 
+/* ------------------------------------------------------------ paged cache ---
+ *
+ * A paged cache holds the same quantised tokens as a kivi_cache, for a batch
+ * whose sequences have lengths of their own.  A page is ONE key-group record
+ * of the history layout above (G tokens of one kv head); a pool of num_pages
+ * records serves every (sequence, kv head) pair, and the pair's table row
+ * names its pages, oldest first.  The state of the sequences is on the
+ * device, so that a captured graph of these calls stays right as they grow.
+ *
+ *    table      int32 [P][C], C = kivi_paged_columns = capacity_tokens / G:
+ *               the page numbers of every pair.  A row names every page the
+ *               pair may use: the ones it holds first, then free ones, which
+ *               the next flushes fill.  No page may be named twice among the
+ *               pages that appends can still fill.
+ *    n_tokens   int32 [B]: tokens the sequence has seen (sink, quantised,
+ *               evicted and window tokens together)
+ *    n_evicted  int32 [B]: pages each of its kv heads has lost to eviction
+ *    k_fp16, v_fp16  as in kivi_cache: sink rows, then the window's ring
+ *    control    kivi_paged_control_bytes bytes, zeroed once: a status word
+ *               (error bits the kernels OR in), then counters
+ *
+ * From n = n_tokens follow, for N_s sink tokens and m = max(n - N_s, 0):
+ *    flushed groups  F = (m > 0 ? (m - 1) / R : 0) R / G   (KIVI_FLUSH_WINDOW)
+ *                    F = m > R ? ceil((m - R) / G) : 0     (KIVI_FLUSH_GROUP)
+ *    pages held      F - n_evicted (columns 0 .. F - n_evicted - 1)
+ *    window          m - F G tokens, the oldest in slot (F G) mod R
+ * which is the state kivi_quantize_prefill keeps on the host, so a kivi_cache
+ * becomes a paged one with the table p C + j over its history buffer.
+ *
+ * Every function here is asynchronous, allocates nothing, synchronises with
+ * nothing and may be captured into a graph.  Calls that read or change one
+ * cache, and calls that share a workspace, must be ordered (one stream, or
+ * events); graphs that share a workspace must not run at once.  Host
+ * arguments are checked before anything is launched.  What only the device
+ * can see is checked there and reported in the status word:
+ *    KIVI_STATUS_BAD_STATE  offsets not ascending or outside 0..num_tokens, a
+ *                           sequence with more than max_new new tokens, or
+ *                           lengths that do not fit the table: the sequence is
+ *                           skipped (its outputs and state stay as they are)
+ *    KIVI_STATUS_BAD_PAGE   a page number outside the pool: nothing is read or
+ *                           written there (its keys and values count as zero),
+ *                           the sequence's result is not valid
+ *    KIVI_STATUS_CAPACITY   an append that needs more than C columns: the
+ *                           sequence is skipped
+ * The pages' contents are not checked: infinities or NaN in a sequence's own
+ * keys, values or queries may reach any output row of that sequence, and of no
+ * other. */
+#define KIVI_STATUS_BAD_STATE 2u
+#define KIVI_STATUS_BAD_PAGE 4u
+#define KIVI_STATUS_CAPACITY 8u
+
+typedef struct kivi_paged {
+    kivi_params p;
+    void *pool;               /* num_pages records                            */
+    void *k_fp16;
+    void *v_fp16;
+    int32_t *table;
+    int32_t *n_tokens;
+    int32_t *n_evicted;
+    uint32_t *control;
+    int64_t num_pages;        /* 1 .. 2^31 - 1                                */
+    uint64_t kernel_launches; /* kernels enqueued on its behalf (informational) */
+} kivi_paged;
+
+/* Which of the new tokens a new token sees (it sees every cached token). */
+enum kivi_mask {
+    KIVI_MASK_CAUSAL = 0,     /* itself and the ones before it                */
+    KIVI_MASK_FULL = 1        /* all of its sequence's (a prefix read at once) */
+};
+
+/* New tokens of a ragged batch.  Sequence b owns the tokens offsets[b] ..
+ * offsets[b + 1] - 1 (none is legal); tokens outside every sequence are never
+ * read or written.  Token i's query head h starts at q + (i q_stride + h d)
+ * halves, its kv head h at k + (i kv_stride + h d); the strides are multiples
+ * of 8 and at least Hq d and Hkv d, so q, k and v may be slices of one
+ * projection's output.  k and v may both be null (attention and weights):
+ * the queries then see the cached tokens alone. */
+typedef struct kivi_chunk {
+    const void *q;            /* fp16; append: null                           */
+    const void *k, *v;        /* fp16; weights: v is not read and may be null */
+    const int32_t *offsets;   /* int32 [B + 1], device                        */
+    int64_t q_stride, kv_stride;   /* elements from token to token            */
+    int64_t num_tokens;       /* tokens the buffers hold                      */
+    int32_t max_new;          /* no sequence has more new tokens than this    */
+    int32_t max_cached;       /* about the longest n_tokens (0: capacity); it
+                                 only steers how the work is split            */
+    float softmax_scale;      /* <= 0: 1 / sqrt(d)                            */
+    float softcap;            /* c > 0: scores become c tanh(score / c);
+                                 <= 0: as they are                            */
+    int32_t mask;             /* enum kivi_mask                               */
+    int32_t reserved;         /* 0                                            */
+} kivi_chunk;
+
+/* Table columns C and bytes of the control buffer; 0 if unsupported.  A paged
+ * cache takes every kivi_params that kivi_params_validate accepts with
+ * capacity_tokens + sink_tokens + residual below 2^31 and at least one column
+ * per pair, C P below 2^31.  Host only. */
+int32_t kivi_paged_columns(const kivi_params *p);
+size_t kivi_paged_control_bytes(const kivi_params *p);
+
+/* Workspace bytes that kivi_paged_attention, kivi_paged_weights and
+ * kivi_paged_evict need for chunks with at most max_new new tokens in one
+ * sequence; 0 if unsupported.  A smaller max_new needs no more.  Contents need
+ * not be initialised; 16-byte aligned.  Host only. */
+size_t kivi_paged_workspace_bytes(const kivi_params *p, int32_t max_new);
+
+/* Bind a paged cache to caller-owned device buffers.  pool, k_fp16 and v_fp16
+ * are 16-byte aligned, the integer arrays 4-byte aligned.  Host only; the
+ * state (n_tokens, n_evicted, control) is the caller's to zero. */
+int kivi_paged_init(kivi_paged *c, const kivi_params *p, void *pool, int64_t num_pages,
+                    void *k_fp16, void *v_fp16, int32_t *table, int32_t *n_tokens,
+                    int32_t *n_evicted, uint32_t *control);
+
+/* Append every sequence's new tokens: what kivi_quantize_prefill does, for a
+ * ragged batch, writing records into the pages the table names.  Updates
+ * n_tokens on the device.  Records are bit-identical to kivi_quantize_prefill's
+ * for the same tokens.  Uses k, v, offsets, kv_stride, num_tokens, max_new. */
+int kivi_paged_append(kivi_paged *c, const kivi_chunk *x, kivi_stream_t stream);
+
+/* Attention of the new tokens (not yet appended) over their sequence's cached
+ * tokens and, as x->mask says, over one another: out fp16
+ * [num_tokens][Hq][d], contiguous.  Rows outside every sequence stay as they
+ * are; a query that sees no token gets zeros.  Reads the cache only. */
+int kivi_paged_attention(kivi_paged *c, const kivi_chunk *x, void *out, void *workspace,
+                         size_t ws_bytes, kivi_stream_t stream);
+
+/* Add to weights, fp32 [P][C], the softmax weight that each page's tokens get
+ * in that attention, summed over the pair's new tokens and query heads
+ * (columns beyond the held pages stay as they are).  The order of the sums is
+ * fixed: equal inputs give equal bits. */
+int kivi_paged_weights(kivi_paged *c, const kivi_chunk *x, float *weights, void *workspace,
+                       size_t ws_bytes, kivi_stream_t stream);
+
+/* Evict pages: a pair that holds n > budget_pages pages keeps the
+ * min(recent_pages, budget_pages) newest ones and, of the others, those with
+ * the largest weights (equal weights: the lower column stays; NaN counts as
+ * the least).  Its table row becomes the kept pages in their order, then the
+ * evicted ones in theirs (the next flushes fill these first; a caller that
+ * shares pages between rows replaces them before it appends), columns from n
+ * on as before.  weights, fp32 [P][C], follows the kept pages; the columns
+ * from budget_pages to n - 1 become 0.  n_evicted grows by n - budget_pages.
+ * No page's contents move. */
+int kivi_paged_evict(kivi_paged *c, float *weights, int32_t budget_pages, int32_t recent_pages,
+                     void *workspace, size_t ws_bytes, kivi_stream_t stream);
+
 /* Static description of a status code. */
 const char *kivi_status_string(int status);
 
@@ -367,6 +512,8 @@ const char *kivi_status_string(int status);
 int kivi_abi_version(void);
 size_t kivi_sizeof_params(void);
 size_t kivi_sizeof_cache(void);
+size_t kivi_sizeof_paged(void);
+size_t kivi_sizeof_chunk(void);
 
 #ifdef __cplusplus
 }

@@ -264,7 +264,7 @@ def prepare(case, seed):
         from bit_kv_cache_06_gb300 import kivi, paged
         shape = kivi.CacheShape(lay.bits, c["G"], c["R"], B, Hq or Hkv, Hkv, D, cols * c["G"], c["sink"], c["meta"],
                                 kivi.KIVI_FLUSH_WINDOW, lay.fmt, K8, V8)
-        st["cache"] = paged.KiviPagedCache(shape, num_pages, max_tokens=N, max_new=max(new), max_cached=max(ctx),
+        st["cache"] = paged.KiviPagedCache(shape, num_pages, max_new=max(new),
                                            buffers=(pool, k_rows, v_rows, table, st["n_tokens"], st["n_evicted"]))
     return st
 
@@ -293,7 +293,7 @@ def _prepare_evict(c, gen):
         shape = kivi.CacheShape(2, 32, 32, B, c["Hkv"], c["Hkv"], D, cols * 32)
         pool = torch.empty((P * cols, 4096), dtype=torch.uint8, device="cuda")
         rows = torch.empty((P, 32, D), dtype=torch.float16, device="cuda")
-        st["cache"] = paged.KiviPagedCache(shape, P * cols, max_tokens=B, max_new=1,
+        st["cache"] = paged.KiviPagedCache(shape, P * cols, max_new=1,
                                            buffers=(pool, rows, rows.clone(), st["table"], tokens, st["n_evicted"]))
     return st
 

@@ -48,13 +48,11 @@ class KiviPagedCache:
             if num_pages < P * self.columns:
                 raise ValueError(f"{num_pages} pages for {P} rows of {self.columns} columns: "
                                  "hand in a table (buffers=) that says which pages a row uses")
-            self.device = torch.device(device)
-            buffers = [torch.empty(s, dtype=t, device=self.device) for _, s, t in want[:3]]
+            buffers = [torch.empty(s, dtype=t, device=device) for _, s, t in want[:3]]
             buffers.append(torch.arange(P * self.columns, dtype=torch.int32,
-                                        device=self.device).view(P, self.columns))
-            buffers += [torch.zeros(B, dtype=torch.int32, device=self.device) for _ in range(2)]
-        else:
-            self.device = buffers[0].device
+                                        device=device).view(P, self.columns))
+            buffers += [torch.zeros(B, dtype=torch.int32, device=device) for _ in range(2)]
+        self.device = buffers[0].device
         for t, (name, size, dtype) in zip(buffers, want):
             if tuple(t.shape) != size or t.dtype != dtype or not t.is_contiguous() or \
                     t.device != self.device:
@@ -138,7 +136,7 @@ class KiviPagedCache:
 
     def _chunk(self, q, k, v, offsets, max_new, max_cached, softmax_scale, softcap, causal):
         s = self.shape
-        if offsets.dtype != torch.int32 or offsets.numel() != s.batch + 1 or \
+        if offsets is None or offsets.dtype != torch.int32 or offsets.numel() != s.batch + 1 or \
                 not offsets.is_contiguous() or offsets.device != self.device:
             raise ValueError(f"offsets: contiguous int32 [{s.batch + 1}] on {self.device} is wanted")
         x = kivi.kivi_chunk()

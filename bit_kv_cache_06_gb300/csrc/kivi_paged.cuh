@@ -28,7 +28,7 @@ struct ChunkArgs {
     const int32_t *offsets;           // [B + 1]
     int64_t q_stride, kv_stride;      // halves from token to token
     int64_t num_tokens;
-    int max_new;
+    int max_new, max_cached;          // bounds of one sequence's new and cached tokens
     float scale_log2;                 // softmax scale * log2(e)
     float cap_log2, cap_inv;          // cap * log2(e) and scale / cap; cap_log2 = 0: no cap
     int full;                         // every new token sees all of its sequence's
@@ -80,6 +80,15 @@ __device__ __forceinline__ bool chunk_of(const ChunkArgs &x, int b, int &first, 
     return true;
 }
 
+// Sequence b of an attention or a weights call: its new tokens and its state;
+// false when the call has to skip it.
+__device__ __forceinline__ bool sequence(const PagedArgs &c, const ChunkArgs &x, int b, int &first, int &T,
+                                         PagedState &s)
+{
+    return chunk_of(x, b, first, T) && paged_state(c, b, s) &&
+           s.sink + s.held * c.G + s.window <= x.max_cached;
+}
+
 // Record in column `col` of pair p, or null when the page number is not one of
 // the pool's.
 __device__ __forceinline__ unsigned char *page_record(const PagedArgs &c, int p, int col)
@@ -92,22 +101,23 @@ __device__ __forceinline__ unsigned char *page_record(const PagedArgs &c, int p,
 
 cudaError_t launch_paged_append(const PagedArgs &c, const ChunkArgs &x, cudaStream_t s, int *launches);
 
-// Work split of an attention or a weights call, and where its parts lie in the
-// workspace: fixed by the sizes alone.
-struct AttendPlan {
-    int splits;           // parts of a pair's tokens
-    int row_tiles;        // tiles of query rows of the longest chunk
-    size_t bytes;         // workspace bytes
-};
-AttendPlan attend_plan(const PagedArgs &c, int max_new, int max_cached);
-AttendPlan weights_plan(const PagedArgs &c, int max_new, int max_cached);
+// Workspace bytes, which only grow with max_new and max_cached (both bounds of
+// one sequence), and launches that need no more.
+size_t attention_bytes(const PagedArgs &c, int max_new, int max_cached);
+size_t weights_bytes(const PagedArgs &c, int max_new, int max_cached);
 size_t evict_bytes(const PagedArgs &c);
 
-cudaError_t launch_paged_attention(const PagedArgs &c, const ChunkArgs &x, int max_cached, __half *out,
-                                   void *ws, cudaStream_t s, int *launches);
-cudaError_t launch_paged_weights(const PagedArgs &c, const ChunkArgs &x, int max_cached, float *weights,
-                                 void *ws, cudaStream_t s, int *launches);
+cudaError_t launch_paged_attention(const PagedArgs &c, const ChunkArgs &x, __half *out, void *ws, cudaStream_t s,
+                                   int *launches);
+cudaError_t launch_paged_weights(const PagedArgs &c, const ChunkArgs &x, float *weights, void *ws, cudaStream_t s,
+                                 int *launches);
 cudaError_t launch_paged_evict(const PagedArgs &c, float *weights, int budget, int recent, void *ws,
                                cudaStream_t s, int *launches);
+
+// The attention of long chunks (kivi_paged_tc.cu).
+bool is_long_chunk(const PagedArgs &c, int max_new);
+size_t long_chunk_bytes(const PagedArgs &c, int max_new, int max_cached);
+cudaError_t launch_long_chunk(const PagedArgs &c, const ChunkArgs &x, __half *out, void *ws, cudaStream_t s,
+                              int *launches);
 
 }  // namespace kivi

@@ -114,6 +114,13 @@ int check_chunk(const kivi_paged *c, const kivi_chunk *x, int uses)
     return KIVI_OK;
 }
 
+// The bound on cached tokens a call goes by: the caller's, or what the table holds.
+int cached_bound(const PagedArgs &a, int max_cached)
+{
+    const int64_t most = (int64_t)a.columns * a.G + a.rows;
+    return (int)(max_cached > 0 ? std::min<int64_t>(max_cached, most) : most);
+}
+
 ChunkArgs chunk_args(const kivi_paged *c, const kivi_chunk *x)
 {
     ChunkArgs a{};
@@ -125,6 +132,7 @@ ChunkArgs chunk_args(const kivi_paged *c, const kivi_chunk *x)
     a.kv_stride = x->kv_stride;
     a.num_tokens = x->num_tokens;
     a.max_new = (int)std::min<int64_t>(x->max_new, x->num_tokens);
+    a.max_cached = cached_bound(paged_args(&c->p), x->max_cached);
     const float scale = x->softmax_scale > 0.0f ? x->softmax_scale : 1.0f / std::sqrt((float)c->p.head_dim);
     a.scale_log2 = scale * 1.4426950408889634f;
     if (x->softcap > 0.0f) {
@@ -137,22 +145,23 @@ ChunkArgs chunk_args(const kivi_paged *c, const kivi_chunk *x)
     return a;
 }
 
-size_t workspace_bytes(const kivi_params *p, int max_new)
+size_t workspace_bytes(const PagedArgs &a, int max_new, int max_cached)
 {
-    const PagedArgs a = paged_args(p);
     size_t n = evict_bytes(a);
     if (max_new > 0) {
-        n = std::max(n, attend_plan(a, max_new, 0).bytes);
-        n = std::max(n, weights_plan(a, max_new, 0).bytes);
+        const int most = cached_bound(a, max_cached);
+        n = std::max(n, attention_bytes(a, max_new, most));
+        n = std::max(n, weights_bytes(a, max_new, most));
+        n = std::max(n, long_chunk_bytes(a, max_new, most));
     }
     return (n + 255) / 256 * 256;
 }
 
-int check_workspace(const kivi_paged *c, int max_new, const void *ws, size_t bytes)
+int check_workspace(const PagedArgs &a, int max_new, int max_cached, const void *ws, size_t bytes)
 {
     if (!ws || !aligned(ws, 16))
         return KIVI_ERR_INVALID_ARG;
-    return bytes < workspace_bytes(&c->p, max_new) ? KIVI_ERR_WORKSPACE : KIVI_OK;
+    return bytes < workspace_bytes(a, max_new, max_cached) ? KIVI_ERR_WORKSPACE : KIVI_OK;
 }
 
 int done(kivi_paged *c, cudaError_t e, int launches)
@@ -175,9 +184,10 @@ size_t kivi_paged_control_bytes(const kivi_params *p)
     return check_paged_params(p) == KIVI_OK ? (4 * (size_t)(1 + p->batch) + 255) / 256 * 256 : 0;
 }
 
-size_t kivi_paged_workspace_bytes(const kivi_params *p, int32_t max_new)
+size_t kivi_paged_workspace_bytes(const kivi_params *p, int32_t max_new, int32_t max_cached)
 {
-    return check_paged_params(p) == KIVI_OK && max_new >= 0 ? workspace_bytes(p, max_new) : 0;
+    return check_paged_params(p) == KIVI_OK && max_new >= 0 && max_cached >= 0
+               ? workspace_bytes(paged_args(p), max_new, max_cached) : 0;
 }
 
 int kivi_paged_init(kivi_paged *c, const kivi_params *p, void *pool, int64_t num_pages, void *k_fp16,
@@ -232,12 +242,13 @@ int kivi_paged_attention(kivi_paged *c, const kivi_chunk *x, void *out, void *wo
     if (!out || !aligned(out, 16))
         return KIVI_ERR_INVALID_ARG;
     const ChunkArgs a = chunk_args(c, x);
-    st = check_workspace(c, a.max_new, workspace, ws_bytes);
+    const PagedArgs pa = paged_args(c);
+    st = check_workspace(pa, a.max_new, x->max_cached, workspace, ws_bytes);
     if (st != KIVI_OK)
         return st;
     int launches = 0;
-    const cudaError_t e = launch_paged_attention(paged_args(c), a, x->max_cached, static_cast<__half *>(out),
-                                                 workspace, reinterpret_cast<cudaStream_t>(stream), &launches);
+    const cudaError_t e = launch_paged_attention(pa, a, static_cast<__half *>(out), workspace,
+                                                 reinterpret_cast<cudaStream_t>(stream), &launches);
     return done(c, e, launches);
 }
 
@@ -255,12 +266,13 @@ int kivi_paged_weights(kivi_paged *c, const kivi_chunk *x, float *weights, void 
     if (x->max_new == 0 || x->num_tokens == 0)
         return KIVI_OK;
     const ChunkArgs a = chunk_args(c, x);
-    st = check_workspace(c, a.max_new, workspace, ws_bytes);
+    const PagedArgs pa = paged_args(c);
+    st = check_workspace(pa, a.max_new, x->max_cached, workspace, ws_bytes);
     if (st != KIVI_OK)
         return st;
     int launches = 0;
-    const cudaError_t e = launch_paged_weights(paged_args(c), a, x->max_cached, weights, workspace,
-                                               reinterpret_cast<cudaStream_t>(stream), &launches);
+    const cudaError_t e = launch_paged_weights(pa, a, weights, workspace, reinterpret_cast<cudaStream_t>(stream),
+                                               &launches);
     return done(c, e, launches);
 }
 
@@ -273,11 +285,12 @@ int kivi_paged_evict(kivi_paged *c, float *weights, int32_t budget_pages, int32_
         return st;
     if (!weights || !aligned(weights, 4) || budget_pages < 0 || recent_pages < 0)
         return KIVI_ERR_INVALID_ARG;
-    st = check_workspace(c, 0, workspace, ws_bytes);
+    const PagedArgs pa = paged_args(c);
+    st = check_workspace(pa, 0, 0, workspace, ws_bytes);
     if (st != KIVI_OK)
         return st;
     int launches = 0;
-    const cudaError_t e = launch_paged_evict(paged_args(c), weights, budget_pages, recent_pages, workspace,
+    const cudaError_t e = launch_paged_evict(pa, weights, budget_pages, recent_pages, workspace,
                                              reinterpret_cast<cudaStream_t>(stream), &launches);
     return done(c, e, launches);
 }

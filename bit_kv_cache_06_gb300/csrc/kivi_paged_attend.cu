@@ -49,7 +49,7 @@ __global__ void __launch_bounds__(kAttendThreads) attend_kernel(PagedArgs c, Chu
     const int p = blockIdx.y, b = p / c.Hkv, h = p % c.Hkv;
     int first, T;
     PagedState st;
-    if (!chunk_of(x, b, first, T) || !paged_state(c, b, st)) {
+    if (!sequence(c, x, b, first, T, st)) {
         if (tid == 0 && blockIdx.x == 0 && blockIdx.z == 0)
             atomicOr(c.control, KIVI_STATUS_BAD_STATE);
         return;
@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(128) join_kernel(PagedArgs c, ChunkArgs x, Spl
     const int p = blockIdx.y, b = p / c.Hkv, h = p % c.Hkv;
     int first, T;
     PagedState st;
-    if (!chunk_of(x, b, first, T) || !paged_state(c, b, st))
+    if (!sequence(c, x, b, first, T, st))
         return;
     const int row = blockIdx.x * 4 + warp;
     if (row >= T * c.g)
@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(128) weigh_kernel(PagedArgs c, ChunkArgs x, Sp
     const int p = blockIdx.y, b = p / c.Hkv;
     int first, T;
     PagedState st;
-    if (!chunk_of(x, b, first, T) || !paged_state(c, b, st))
+    if (!sequence(c, x, b, first, T, st))
         return;
     const int rows = min(d.rows, T * c.g - d.row0);
     const int col = blockIdx.x * 128 + threadIdx.x;
@@ -373,11 +373,9 @@ void launch_attend(const PagedArgs &c, const ChunkArgs &x, const SplitOut &d, di
 
 // Splits that fill the GPU: the blocks of one split are `blocks`, and no split
 // is shorter than two tiles of the longest sequence.
-int split_count(const PagedArgs &c, int64_t blocks, int max_new, int max_cached)
+int split_count(int64_t blocks, int max_new, int max_cached)
 {
-    const int64_t cap = (int64_t)c.columns * c.G + c.rows;
-    const int64_t tokens = (max_cached > 0 && max_cached < cap ? max_cached : cap) + max_new;
-    const int64_t tiles = (tokens + kTile - 1) / kTile;
+    const int64_t tiles = ((int64_t)max_cached + max_new + kTile - 1) / kTile;
     return (int)std::max<int64_t>(1, std::min((kTargetBlocks + blocks - 1) / blocks, tiles / 2));
 }
 
@@ -385,38 +383,59 @@ constexpr int64_t kWeighBytes = 256ll << 20;     // rows of page sums held at on
 
 }  // namespace
 
-AttendPlan attend_plan(const PagedArgs &c, int max_new, int max_cached)
+namespace {
+
+struct Plan {
+    int splits;           // parts of a pair's tokens
+    int row_tiles;        // tiles of query rows of the longest chunk, or of one launch
+};
+
+Plan attend_plan(const PagedArgs &c, int max_new, int max_cached)
 {
     const int64_t pairs = (int64_t)c.B * c.Hkv;
-    AttendPlan p;
+    Plan p;
     p.row_tiles = (int)(((int64_t)max_new * c.g + kTile - 1) / kTile);
-    p.splits = split_count(c, pairs * p.row_tiles, max_new, max_cached);
-    // splits * rows <= 64 (blocks + target), and more rows mean one split
-    const int64_t blocks = std::min<int64_t>(pairs * p.row_tiles, kTargetBlocks);
-    p.bytes = (size_t)(kTile * (blocks + kTargetBlocks)) * (kHeadDim + 2) * 4;
+    p.splits = split_count(pairs * p.row_tiles, max_new, max_cached);
     return p;
 }
 
-static int weigh_unit(const PagedArgs &c) { return std::min(c.G, kTile); }
+int weigh_unit(const PagedArgs &c) { return std::min(c.G, kTile); }
 
-// row_tiles: query row tiles per launch
-AttendPlan weights_plan(const PagedArgs &c, int max_new, int max_cached)
+Plan weights_plan(const PagedArgs &c, int max_new, int max_cached)
 {
     const int64_t pairs = (int64_t)c.B * c.Hkv;
     const int64_t units = (int64_t)c.columns * c.G / weigh_unit(c);
     const int64_t all = ((int64_t)max_new * c.g + kTile - 1) / kTile;
-    AttendPlan p;
+    Plan p;
     p.row_tiles = (int)std::max<int64_t>(1, std::min(all, kWeighBytes / (pairs * kTile * units * 4)));
-    p.splits = split_count(c, pairs * p.row_tiles, max_new, max_cached);
-    const int64_t rows = pairs * p.row_tiles * kTile;
-    p.bytes = (size_t)rows * units * 4 + (size_t)kTile * (pairs * p.row_tiles + kTargetBlocks) * 8;
+    p.splits = split_count(pairs * p.row_tiles, max_new, max_cached);
     return p;
 }
 
-cudaError_t launch_paged_attention(const PagedArgs &c, const ChunkArgs &x, int max_cached, __half *out,
-                                   void *ws, cudaStream_t s, int *launches)
+}  // namespace
+
+size_t attention_bytes(const PagedArgs &c, int max_new, int max_cached)
 {
-    const AttendPlan p = attend_plan(c, x.max_new, max_cached);
+    // splits * blocks < blocks + target, and more blocks than that mean one split
+    const int64_t blocks = std::min<int64_t>((int64_t)c.B * c.Hkv * attend_plan(c, max_new, max_cached).row_tiles,
+                                             kTargetBlocks);
+    return (size_t)(kTile * (blocks + kTargetBlocks)) * (kHeadDim + 2) * 4;
+}
+
+size_t weights_bytes(const PagedArgs &c, int max_new, int max_cached)
+{
+    const int64_t pairs = (int64_t)c.B * c.Hkv;
+    const int64_t units = (int64_t)c.columns * c.G / weigh_unit(c);
+    const int64_t tiles = pairs * weights_plan(c, max_new, max_cached).row_tiles;
+    return (size_t)tiles * kTile * units * 4 + (size_t)kTile * (tiles + kTargetBlocks) * 8;
+}
+
+cudaError_t launch_paged_attention(const PagedArgs &c, const ChunkArgs &x, __half *out, void *ws, cudaStream_t s,
+                                   int *launches)
+{
+    if (is_long_chunk(c, x.max_new))
+        return launch_long_chunk(c, x, out, ws, s, launches);
+    const Plan p = attend_plan(c, x.max_new, x.max_cached);
     const int pairs = c.B * c.Hkv;
     SplitOut d{};
     d.out = out;
@@ -434,10 +453,10 @@ cudaError_t launch_paged_attention(const PagedArgs &c, const ChunkArgs &x, int m
     return cudaGetLastError();
 }
 
-cudaError_t launch_paged_weights(const PagedArgs &c, const ChunkArgs &x, int max_cached, float *weights,
-                                 void *ws, cudaStream_t s, int *launches)
+cudaError_t launch_paged_weights(const PagedArgs &c, const ChunkArgs &x, float *weights, void *ws, cudaStream_t s,
+                                 int *launches)
 {
-    const AttendPlan p = weights_plan(c, x.max_new, max_cached);
+    const Plan p = weights_plan(c, x.max_new, x.max_cached);
     const int pairs = c.B * c.Hkv;
     SplitOut d{};
     d.S = p.splits;

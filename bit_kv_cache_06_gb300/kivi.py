@@ -142,7 +142,7 @@ def load(path: str = LIB_PATH):
         "kivi_test_decode_wait_timeout": (ctypes.c_int, [C, vp, vp, vp, sz, vp]),
         "kivi_paged_columns": (i32, [P]),
         "kivi_paged_control_bytes": (sz, [P]),
-        "kivi_paged_workspace_bytes": (sz, [P, i32]),
+        "kivi_paged_workspace_bytes": (sz, [P, i32, i32]),
         "kivi_paged_init": (ctypes.c_int, [PC, P, vp, i64] + [vp] * 6),
         "kivi_paged_append": (ctypes.c_int, [PC, X, vp]),
         "kivi_paged_attention": (ctypes.c_int, [PC, X, vp, vp, sz, vp]),

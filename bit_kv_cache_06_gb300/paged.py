@@ -24,11 +24,13 @@ class KiviPagedCache:
     [B], all contiguous on one device.  Allocated tables hold the pages in
     order (row p: p C .. p C + C - 1), which needs num_pages = P C or more.
 
-    max_new: the longest chunk one sequence will bring in a call of attention
-    or weights; it sizes the workspace (which layers may share: workspace=,
-    for calls that are ordered on the GPU).  A longer one is refused."""
+    max_new, max_cached: the longest chunk one sequence will bring in a call of
+    attention or weights, and the most cached tokens it will then hold (0: as
+    many as the table does).  They size the workspace (which layers may share:
+    workspace=, for calls that are ordered on the GPU); longer ones are refused."""
 
-    def __init__(self, shape, num_pages=None, max_new=1, device="cuda", buffers=None, workspace=None):
+    def __init__(self, shape, num_pages=None, max_new=1, max_cached=0, device="cuda", buffers=None,
+                 workspace=None):
         L = kivi.load()
         self.shape = shape
         self.params = shape.params()
@@ -59,8 +61,8 @@ class KiviPagedCache:
                 raise ValueError(f"{name}: {dtype} {list(size)}, contiguous, on {self.device} is wanted; "
                                  f"got {t.dtype} {list(t.shape)} on {t.device}")
         self.pool, self.k_fp16, self.v_fp16, self.table, self.n_tokens, self.n_evicted = buffers
-        self.max_new = int(max_new)
-        need = L.kivi_paged_workspace_bytes(ctypes.byref(self.params), self.max_new)
+        self.max_new, self.max_cached = int(max_new), int(max_cached)
+        need = L.kivi_paged_workspace_bytes(ctypes.byref(self.params), self.max_new, self.max_cached)
         if need == 0:
             raise kivi.KiviError(kivi.KIVI_ERR_UNSUPPORTED, "kivi_paged_workspace_bytes")
         if workspace is None:
@@ -82,7 +84,7 @@ class KiviPagedCache:
         self._c = ctypes.byref(self.c)
 
     @classmethod
-    def from_cache(cls, cache, max_new=1, workspace=None):
+    def from_cache(cls, cache, max_new=1, max_cached=0, workspace=None):
         """A paged view of a KiviCache as it is now: its history buffer is the
         pool, row p names records p C .. p C + C - 1, every sequence has the
         cache's length.  The two share buffers, not state: tokens appended to
@@ -94,7 +96,7 @@ class KiviPagedCache:
         table = torch.arange(P * C, dtype=torch.int32, device=cache.device).view(P, C)
         n = cache.n_sink + cache.n_quant + cache.n_resid
         tokens = torch.full((s.batch,), n, dtype=torch.int32, device=cache.device)
-        return cls(s, P * C, max_new, buffers=(pool, cache.view("k_fp16"), cache.view("v_fp16"), table,
+        return cls(s, P * C, max_new, max_cached, buffers=(pool, cache.view("k_fp16"), cache.view("v_fp16"), table,
                                                tokens, torch.zeros_like(tokens)), workspace=workspace)
 
     # ---- state ------------------------------------------------------------
@@ -156,7 +158,7 @@ class KiviPagedCache:
         x.offsets = offsets.data_ptr()
         x.num_tokens = n
         x.max_new = n if max_new is None else int(max_new)
-        x.max_cached = int(max_cached)
+        x.max_cached = self.max_cached if max_cached is None else int(max_cached)
         x.softmax_scale, x.softcap = float(softmax_scale), float(softcap)
         x.mask = kivi.KIVI_MASK_CAUSAL if causal else kivi.KIVI_MASK_FULL
         return x
@@ -179,13 +181,14 @@ class KiviPagedCache:
             _check(kivi.load().kivi_paged_append(self._c, ctypes.byref(x), s.cuda_stream),
                    "kivi_paged_append")
 
-    def attention(self, q, k=None, v=None, offsets=None, max_new=None, max_cached=0, softmax_scale=0.0,
+    def attention(self, q, k=None, v=None, offsets=None, max_new=None, max_cached=None, softmax_scale=0.0,
                   softcap=0.0, causal=True, out=None, stream=None):
         """Attention of new tokens q fp16 [N, Hq, d] over their sequence's
         cached tokens and over k, v fp16 [N, Hkv, d] of the new tokens
         themselves (causally, or all of them with causal=False; without k, v
-        over the cached tokens alone).  Appends nothing.  max_cached, about
-        the longest n_tokens, steers the split of the work.  Returns out, fp16
+        over the cached tokens alone).  Appends nothing.  max_cached bounds
+        the cached tokens of any sequence (default: the cache's); the nearer
+        it is, the better the work is split.  Returns out, fp16
         [N, Hq, d]; rows outside every sequence stay as they are."""
         x = self._chunk(q, k, v, offsets, max_new, max_cached, softmax_scale, softcap, causal)
         with torch.cuda.device(self.device):
@@ -201,7 +204,7 @@ class KiviPagedCache:
                                                     s.cuda_stream), "kivi_paged_attention")
         return out
 
-    def weights(self, weights, q, k=None, offsets=None, max_new=None, max_cached=0, softmax_scale=0.0,
+    def weights(self, weights, q, k=None, offsets=None, max_new=None, max_cached=None, softmax_scale=0.0,
                 softcap=0.0, causal=True, stream=None):
         """Add to weights, fp32 [P, C], what each page gets of the softmax
         weights of `attention`'s queries."""

@@ -396,8 +396,9 @@ int kivi_test_decode_wait_timeout(kivi_cache *c, const void *q, void *out,
  * arguments are checked before anything is launched.  What only the device
  * can see is checked there and reported in the status word:
  *    KIVI_STATUS_BAD_STATE  offsets not ascending or outside 0..num_tokens, a
- *                           sequence with more than max_new new tokens, or
- *                           lengths that do not fit the table: the sequence is
+ *                           sequence with more than max_new new or
+ *                           max_cached cached tokens, or lengths that do not
+ *                           fit the table: the sequence is
  *                           skipped (its outputs and state stay as they are)
  *    KIVI_STATUS_BAD_PAGE   a page number outside the pool: nothing is read or
  *                           written there (its keys and values count as zero),
@@ -444,8 +445,9 @@ typedef struct kivi_chunk {
     int64_t q_stride, kv_stride;   /* elements from token to token            */
     int64_t num_tokens;       /* tokens the buffers hold                      */
     int32_t max_new;          /* no sequence has more new tokens than this    */
-    int32_t max_cached;       /* about the longest n_tokens (0: capacity); it
-                                 only steers how the work is split            */
+    int32_t max_cached;       /* attention, weights: no sequence has more
+                                 cached tokens (sink, pages, window) than
+                                 this; 0: as many as the table holds          */
     float softmax_scale;      /* <= 0: 1 / sqrt(d)                            */
     float softcap;            /* c > 0: scores become c tanh(score / c);
                                  <= 0: as they are                            */
@@ -462,9 +464,10 @@ size_t kivi_paged_control_bytes(const kivi_params *p);
 
 /* Workspace bytes that kivi_paged_attention, kivi_paged_weights and
  * kivi_paged_evict need for chunks with at most max_new new tokens in one
- * sequence; 0 if unsupported.  A smaller max_new needs no more.  Contents need
- * not be initialised; 16-byte aligned.  Host only. */
-size_t kivi_paged_workspace_bytes(const kivi_params *p, int32_t max_new);
+ * sequence and at most max_cached cached ones (0: as many as the table
+ * holds); 0 if unsupported.  Calls with less of either need no more.  Contents
+ * need not be initialised; 16-byte aligned.  Host only. */
+size_t kivi_paged_workspace_bytes(const kivi_params *p, int32_t max_new, int32_t max_cached);
 
 /* Bind a paged cache to caller-owned device buffers.  pool, k_fp16 and v_fp16
  * are 16-byte aligned, the integer arrays 4-byte aligned.  Host only; the

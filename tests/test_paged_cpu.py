@@ -57,10 +57,13 @@ def test_sizes(L):
     assert col(batch=4096, num_kv_heads=8, num_q_heads=8, capacity_tokens=1 << 21) == 0   # C P above 2^31
     assert L.kivi_paged_control_bytes(ctypes.byref(params())) == 256
     assert L.kivi_paged_control_bytes(ctypes.byref(params(batch=64))) == 512
-    sizes = [L.kivi_paged_workspace_bytes(ctypes.byref(params()), n) for n in (0, 1, 2, 17, 100, 1000, 5000)]
+    sizes = [L.kivi_paged_workspace_bytes(ctypes.byref(params()), n, 0) for n in (0, 1, 2, 17, 100, 1000, 5000)]
     assert sizes == sorted(sizes) and sizes[0] >= 4 * 128 * 4 and all(s % 256 == 0 for s in sizes)
-    assert L.kivi_paged_workspace_bytes(ctypes.byref(params()), -1) == 0
-    assert L.kivi_paged_workspace_bytes(ctypes.byref(params(bits=3)), 1) == 0
+    assert L.kivi_paged_workspace_bytes(ctypes.byref(params()), -1, 0) == 0
+    assert L.kivi_paged_workspace_bytes(ctypes.byref(params()), 1, -1) == 0
+    assert L.kivi_paged_workspace_bytes(ctypes.byref(params(bits=3)), 1, 0) == 0
+    sizes = [L.kivi_paged_workspace_bytes(ctypes.byref(params()), 1000, n) for n in (1, 64, 1000, 4000, 0)]
+    assert sizes == sorted(sizes)
 
 
 def test_init_refuses(L):

@@ -125,23 +125,23 @@ def test_chunk_lengths(counts):
         fill(m, [333])
         m.chunk(counts)
         attend(m)
-        attend(m, softmax_scale=0.0, max_cached=1)     # a poor hint costs time, not correctness
+        attend(m, softmax_scale=0.0, max_cached=333)   # a tight bound, another split
 
 
-def test_long_cache_and_split_hints():
-    """20000 cached tokens: many splits, one split, any hint -- the same rows."""
+def test_long_cache_and_bounds():
+    """20000 cached tokens: many splits, and any bound that holds."""
     m = Model(1, 1, 4, seed=6, columns=640, max_new=300, R=128)
     for _ in range(20):
         fill(m, [1000])
     for counts in ([1], [4], [40], [300]):
         m.chunk(counts)
         want, tol = m.attention()
-        for hint in (0, 1, 20000):
+        for hint in (0, 20000, 20001):
             x = m.dev
             close(m.gpu.attention(x["q"], x["k"], x["v"], x["offsets"], x["max_new"], max_cached=hint)[:counts[0]],
                   want, tol, f"{counts} {hint}")
         ref, wt = m.weights()
-        for hint in (0, 1, 20000):
+        for hint in (0, 20000, 20001):
             w = torch.zeros((1, m.columns), device="cuda")
             m.gpu.weights(w, x["q"], x["k"], x["offsets"], x["max_new"], max_cached=hint)
             close(w, ref, wt, f"weights {counts} {hint}")
@@ -246,7 +246,7 @@ def test_a_serving_run(kw):
     for step in range(5):
         for counts in ([150, 40, 0], [1, 1, 1], [3, 1, 20]):
             x = m.chunk(counts)
-            attend(m, max_cached=200)
+            attend(m, max_cached=m.columns * m.G + m.sink + m.R)
             before = w.clone()
             m.gpu.weights(w, x["q"], x["k"], x["offsets"], x["max_new"])
             close(w, *m.weights(base=before.cpu()), "weights")
@@ -419,6 +419,13 @@ def test_bad_lengths_skip_their_sequence_alone():
         assert [b for b in range(3) if grown[b]] == fine
         for t, s in zip((m.gpu.pool, m.gpu.k_fp16, m.gpu.v_fp16), state):
             t.copy_(s)
+    # more cached tokens than max_cached says, in every sequence
+    m.gpu.n_tokens.copy_(tokens)
+    m.gpu.n_evicted.copy_(gone)
+    m.gpu.control.zero_()
+    out = torch.full_like(x["q"].contiguous(), 7.0)
+    m.gpu.attention(x["q"], x["k"], x["v"], off, 10, max_cached=99, out=out)
+    assert (out == 7.0).all() and m.gpu.status() == kivi.KIVI_STATUS_BAD_STATE
     # more new tokens than max_new says, in every sequence
     m.gpu.n_tokens.copy_(tokens)
     m.gpu.n_evicted.copy_(gone)

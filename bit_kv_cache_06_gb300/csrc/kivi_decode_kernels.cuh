@@ -42,9 +42,16 @@
 //    slices through a private cp.async.bulk pipeline (mbarrier completion,
 //    bounded waits), so the main loop has no block-wide barrier.
 //  * decode_split_simt: CUDA cores, fp32 throughout (G = 16 and reference).
+//
+// decode_split_mma also serves the paged cache (PG = 1: attention of a few
+// query rows per pair; PG = 2: the pages' softmax sums, keys alone): the
+// sequence's state then comes from the device, a block takes GQ query rows
+// (token r / g, head r mod g) of its pair, records are found through the page
+// table, the new tokens follow the fp16 rows with their mask, and scores may be
+// capped.
 #pragma once
 
-#include "kivi_internal.cuh"
+#include "kivi_paged_decode.cuh"
 
 #include <atomic>
 #include <type_traits>
@@ -713,6 +720,13 @@ __device__ __forceinline__ uint32_t hmul2_u32(uint32_t x, __half2 f)
     return *reinterpret_cast<uint32_t *>(&h);
 }
 
+// x rounded to fp16 values (packed in h as pack_f16 does), as floats.
+__device__ __forceinline__ float2 round_f16(float2 x, uint32_t &h)
+{
+    h = pack_f16(x.x, x.y);
+    return __half22float2(*reinterpret_cast<const __half2 *>(&h));
+}
+
 template <int BITS, int G, int GQ, int MF, int F8 = 0>
 struct MmaCfg {
     using RC = Rec<BITS, G, MF>;
@@ -765,8 +779,9 @@ struct MmaCfg {
 // codes -- each warp takes 16-token tiles of the block's range, converts the
 // fp8 rows to fp16 while staging them and runs them through the same tile
 // path as the fp16 rows (BITS, G only size the per-warp buffers then).
-template <int BITS, int G, int GQ, int MF, int F8 = 0>
-__global__ void __launch_bounds__(kThreads, 3) decode_split_mma(DecodeArgs a)
+template <int BITS, int G, int GQ, int MF, int F8 = 0, int PG = 0>
+__global__ void __launch_bounds__(kThreads, 3)
+    decode_split_mma(typename std::conditional<PG != 0, PagedDecodeArgs, DecodeArgs>::type arg)
 {
     using C = MmaCfg<BITS, G, GQ, MF, F8>;
     using RC = typename C::RC;
@@ -780,12 +795,56 @@ __global__ void __launch_bounds__(kThreads, 3) decode_split_mma(DecodeArgs a)
     const int p = blockIdx.y;
     __shared__ int s_last;
     __shared__ int s_failed;          // a warp's bounded wait gave up
+    [[maybe_unused]] DecodeArgs local;            // paged: with the state of this block's sequence
+    [[maybe_unused]] int prow0 = 0, row0 = 0;     // paged: first query row, in the chunk launch and in the pair
+    [[maybe_unused]] int first = 0, cached16 = 0; // paged: first new token, fp16 tokens that are cached
+    if constexpr (PG != 0) {
+        PagedState ps;
+        int T;
+        if (!sequence(arg.c, arg.x, p / arg.c.Hkv, first, T, ps)) {
+            if (tid == 0 && split == 0 && blockIdx.z == 0)
+                atomicOr(arg.c.control, KIVI_STATUS_BAD_STATE);
+            return;
+        }
+        prow0 = blockIdx.z * GQ;
+        row0 = arg.row0 + prow0;
+        if (row0 >= T * arg.c.g)
+            return;
+        local = arg.d;
+        local.g = min(GQ, T * arg.c.g - row0);    // rows of this block
+        local.n_quant = (int64_t)ps.held * G;
+        local.n_sink = ps.sink;
+        local.head = ps.head;
+        cached16 = ps.sink + ps.window;
+        // new tokens that any of the block's rows sees
+        const int seen = !arg.x.k ? 0 : arg.x.full ? T : min(T, (row0 + local.g - 1) / arg.c.g + 1);
+        local.n_fp16 = cached16 + seen;
+    }
+    const DecodeArgs &a = decode_args(arg, local);
     const int b = p / a.Hkv, h = p % a.Hkv;
-    const int64_t qrow0 = (int64_t)b * a.Hkv * a.g + (int64_t)h * a.g;
+    // first row of the partial results
+    const int64_t qrow0 = PG != 0 ? (int64_t)p * paged_rows(arg) + prow0
+                                  : (int64_t)b * a.Hkv * a.g + (int64_t)h * a.g;
+    // query element c of row hh
+    auto query = [&](int hh, int c) -> __half {
+        if constexpr (PG != 0) {
+            const int tok = (row0 + hh) / arg.c.g, head = row0 + hh - tok * arg.c.g;
+            return arg.x.q[(int64_t)(first + tok) * arg.x.q_stride + (h * arg.c.g + head) * D + c];
+        } else {
+            return a.q[(qrow0 + hh) * D + c];
+        }
+    };
     if (tid == 0)
         s_failed = 0;
-    if (split == a.S - 1 && tid == 0)
-        prefetch_residual(a, p);
+    if (split == a.S - 1 && tid == 0) {
+        if constexpr (PG != 0) {
+            DecodeArgs rows = a;
+            rows.n_fp16 = cached16;
+            prefetch_residual(rows, p);
+        } else {
+            prefetch_residual(a, p);
+        }
+    }
     __syncthreads();                  // s_failed is cleared before any wait can set it
 
     // this block's 128-token chunks, as key groups; then this warp's run
@@ -819,13 +878,52 @@ __global__ void __launch_bounds__(kThreads, 3) decode_split_mma(DecodeArgs a)
     // operands).  Sub-slice 0 of a group brings the group's Ks, Kz along.
     // `extra` bytes are expected on top of the copy (the failure-path test
     // hook; 0 otherwise).
+    // Paged: lane k holds the number of the run's page 32 `block` + k.
+    [[maybe_unused]] int ids = 0, ids_block = -1;
+    auto page = [&](int64_t col0, int step, int i) -> const uint8_t * {
+        if constexpr (PG != 0) {
+            if (i >> 5 != ids_block) {
+                ids_block = i >> 5;
+                const int64_t col = col0 + (int64_t)step * (32 * ids_block + lane);
+                ids = col < arg.c.columns ? arg.c.table[(int64_t)p * arg.c.columns + col] : 0;
+            }
+            const int id = __shfl_sync(0xffffffffu, ids, i & 31);
+            return id < 0 || id >= arg.c.num_pages ? nullptr : arg.c.pool + (int64_t)id * (F8 ? 64 * D : RC::BYTES);
+        } else {
+            return nullptr;
+        }
+    };
+    // A page number outside the pool: the stage is zero in its place.
+    auto blank = [&](unsigned char *dst, int bytes, uint32_t bar) {
+        for (int o = 16 * lane; o < bytes; o += 512)
+            *reinterpret_cast<uint4 *>(dst + o) = make_uint4(0u, 0u, 0u, 0u);
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) {
+            atomicOr(a.status, KIVI_STATUS_BAD_PAGE);
+            asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+        }
+    };
     auto issue = [&](int i, bool go, uint32_t extra) {
         const int stage = i % C::STAGES;
         const int sub = UG == 1 ? 0 : i % UG;
-        const uint32_t bytes = sub == 0 ? RC::META + RC::SUB : RC::SUB;
+        constexpr int SUB = PG == 2 ? RC::SL * RB : RC::SUB;    // the weights read the keys alone
+        const uint32_t bytes = sub == 0 ? RC::META + SUB : SUB;
         const uint32_t bar = bar0 + 8 * stage;
         const uint32_t dst = wbase_s + stage * C::STAGE + (sub == 0 ? 0 : RC::META);
-        const uint8_t *src = wrec + (int64_t)(i / UG) * RC::BYTES + (sub == 0 ? 0 : RC::META + sub * RC::SUB);
+        const uint8_t *src;
+        if constexpr (PG != 0) {
+            if (i >= nw)
+                return;
+            const uint8_t *rec = page(wg0, 1, i / UG);
+            if (!rec) {
+                blank(wbase + stage * C::STAGE + (sub == 0 ? 0 : RC::META), (int)bytes, bar);
+                return;
+            }
+            src = rec + (sub == 0 ? 0 : RC::META + sub * RC::SUB);
+        } else {
+            src = wrec + (int64_t)(i / UG) * RC::BYTES + (sub == 0 ? 0 : RC::META + sub * RC::SUB);
+        }
         mbar_expect_tx_if(go, bar, bytes + extra);
         bulk_g2s_hint_if(go, dst, src, bytes, bar, stream_policy);
     };
@@ -845,14 +943,19 @@ __global__ void __launch_bounds__(kThreads, 3) decode_split_mma(DecodeArgs a)
     for (int hh = 0; hh < GQ; ++hh)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            qh[hh][i] = (hh < a.g) ? a.q[(qrow0 + hh) * D + ch[i]] : __float2half(0.0f);
+            qh[hh][i] = (hh < a.g) ? query(hh, ch[i]) : __float2half(0.0f);
     // Only the first sub-slice at the start: the later stages are filled once
     // it has landed, which halves the grid's first burst of copies and with
     // it the wait for the first data.
     if (nw > 0)
         issue(0, lane == 0, poison ? 16u : 0u);
 
-    const int o_k = code_o((BITS == 2) ? 2 * bs : 4 * (bs & 3), BITS);
+    // Weights (fp32 results): a code low in a subnormal's mantissa would cost
+    // up to ten bits of its product, which fp16 outputs do not show but sums of
+    // weights would; one exact multiply per code pair makes it code 2^-10, a
+    // normal number (o = 14), and the query operand is scaled up as much.
+    constexpr int kNormal = 14;
+    const int o_k = PG == 2 ? kNormal : code_o((BITS == 2) ? 2 * bs : 4 * (bs & 3), BITS);
     // q * tau * log2(e) * 2^-o_k: the code operand of this k-step carries 2^o_k
     float qreg[GQ][4];
     float qmax = 0.0f;
@@ -901,14 +1004,16 @@ __global__ void __launch_bounds__(kThreads, 3) decode_split_mma(DecodeArgs a)
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
             const float m_new = fmaxf(m_run[j], mx);
-            alpha[j] = ex2_ftz(m_run[j] - m_new);
+            // paged: a row may see none of a tile's tokens, nor any before it
+            const float m_at = PG != 0 && m_new == -INFINITY ? 0.0f : m_new;
+            alpha[j] = ex2_ftz(m_run[j] - m_at);
             m_run[j] = m_new;
             float sum = 0.0f;
 #pragma unroll
             for (int kt = 0; kt < 2; ++kt)
 #pragma unroll
                 for (int rr = 0; rr < 2; ++rr) {
-                    pr[kt][rr][j] = ex2_ftz(sc[kt][rr][j] - m_new);
+                    pr[kt][rr][j] = ex2_ftz(sc[kt][rr][j] - m_at);
                     sum += pr[kt][rr][j];
                 }
             l_part[j] = fmaf(l_part[j], alpha[j], sum);
@@ -925,6 +1030,50 @@ __global__ void __launch_bounds__(kThreads, 3) decode_split_mma(DecodeArgs a)
 #pragma unroll
             for (int j = 0; j < NH; ++j)
                 zacc[v][j] *= alpha[j];
+    };
+
+    // Paged: cap the scores (log2 units): c tanh(s / c).
+    [[maybe_unused]] auto cap_scores = [&](float (&sc)[2][2][NH], int kts) {
+        if constexpr (PG != 0) {
+            if (arg.x.cap_log2 != 0.0f) {
+#pragma unroll
+                for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+                    for (int rr = 0; rr < 2; ++rr)
+#pragma unroll
+                        for (int j = 0; j < NH; ++j)
+                            if (kt < kts)
+                                sc[kt][rr][j] = arg.x.cap_log2 * tanh_exp(sc[kt][rr][j] * arg.cap_log2_inv);
+            }
+        }
+    };
+    // Weights: log2 of the sum over this unit of tokens (a slice, or an FP8
+    // tile) goes to its place, and the running maximum and sum take it in (the
+    // sum in the lanes of row 0 alone: the epilogue adds the lanes up).
+    [[maybe_unused]] auto weigh_unit = [&](const float (&sc)[2][2][NH], int kts, int64_t unit) {
+        if constexpr (PG == 2) {
+#pragma unroll
+            for (int j = 0; j < NH; ++j) {
+                float mx = fmaxf(sc[0][0][j], sc[0][1][j]);
+                if (kts == 2)
+                    mx = fmaxf(mx, fmaxf(sc[1][0][j], sc[1][1][j]));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+                float sum = ex2_ftz(sc[0][0][j] - mx) + ex2_ftz(sc[0][1][j] - mx);
+                if (kts == 2)
+                    sum += ex2_ftz(sc[1][0][j] - mx) + ex2_ftz(sc[1][1][j] - mx);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+                const int hh = GQ == 4 ? t : 2 * t + j;
+                if (r == 0 && hh < a.g)
+                    arg.ls[(qrow0 + hh) * arg.units + unit] = mx + __log2f(sum);
+                const float m_new = fmaxf(m_run[j], mx);
+                l_part[j] = l_part[j] * ex2_ftz(m_run[j] - m_new) + (r == 0 ? sum * ex2_ftz(mx - m_new) : 0.0f);
+                m_run[j] = m_new;
+            }
+        }
     };
 
     bool failed = false;
@@ -963,12 +1112,26 @@ __global__ void __launch_bounds__(kThreads, 3) decode_split_mma(DecodeArgs a)
         const int nhw = F8 && warp < nht ? (nht - warp + C::NWARP - 1) / C::NWARP : 0;
         auto issue_tile = [&](int j, bool go) {
             const int64_t t0 = h_lo + (int64_t)(warp + C::NWARP * j) * RT;
-            const uint8_t *src = a.hist + ((int64_t)p * (a.cap / 32) + t0 / 32) * (64 * D) + (t0 % 32) * D;
             const uint32_t dst = wbase_s + (j % C::STAGES) * C::STAGE;
             const uint32_t bar = bar0 + 8 * (j % C::STAGES);
-            mbar_expect_tx_if(go, bar, 2 * RT * D);
+            const uint8_t *src;
+            if constexpr (PG != 0) {
+                if (j >= nhw)
+                    return;
+                // tile warp + 4 j lies in page h_lo / 32 + warp / 2 + 2 j
+                const uint8_t *rec = page(h_lo / 32 + warp / 2, 2, j);
+                if (!rec) {
+                    blank(wbase + (j % C::STAGES) * C::STAGE, 2 * RT * D, bar);
+                    return;
+                }
+                src = rec + (t0 % 32) * D;
+            } else {
+                src = a.hist + ((int64_t)p * (a.cap / 32) + t0 / 32) * (64 * D) + (t0 % 32) * D;
+            }
+            mbar_expect_tx_if(go, bar, (PG == 2 ? 1 : 2) * RT * D);
             bulk_g2s_hint_if(go, dst, src, RT * D, bar, stream_policy);
-            bulk_g2s_hint_if(go, dst + RT * D, src + 32 * D, RT * D, bar, stream_policy);
+            if constexpr (PG != 2)
+                bulk_g2s_hint_if(go, dst + RT * D, src + 32 * D, RT * D, bar, stream_policy);
         };
         // bounded wait for tile j; on failure the copies in flight (j .. j +
         // STAGES - 1) get one more bounded wait, as for the packed history
@@ -1010,7 +1173,7 @@ __global__ void __launch_bounds__(kThreads, 3) decode_split_mma(DecodeArgs a)
                     float v[4], hi[4], lo[4];
     #pragma unroll
                     for (int i2 = 0; i2 < 4; ++i2) {
-                        v[i2] = (hh < a.g) ? __half2float(a.q[(qrow0 + hh) * D + cn[i2]]) * a.scale_log2 * fEr : 0.0f;
+                        v[i2] = (hh < a.g) ? __half2float(query(hh, cn[i2])) * a.scale_log2 * fEr : 0.0f;
                         hi[i2] = trunc11(v[i2]);
                         lo[i2] = v[i2] - hi[i2];
                     }
@@ -1032,14 +1195,20 @@ __global__ void __launch_bounds__(kThreads, 3) decode_split_mma(DecodeArgs a)
             const uint32_t tst_s = wbase_s + ((F8 || C::TILES_FIRST) ? C::TSTOFF : 0);
             // 16 rows x 16 chunks of 16 bytes of fp16 tokens t0r ..; rows past
             // the window are zero (their p is 0 and 0 * 0 stays 0)
-            auto stage_rows = [&](const __half *buf, int t0r, int n) {
+            auto stage_rows = [&](const __half *buf, [[maybe_unused]] const __half *fresh, int t0r, int n) {
     #pragma unroll
                 for (int c = lane; c < RT * 16; c += 32) {
                     const int row = c >> 4, col = c & 15;
                     uint4 x = make_uint4(0u, 0u, 0u, 0u);
                     if (row < n) {
-                        const int fr = fp16_row(t0r + row, a.n_sink, a.Ns, a.R, a.head);
-                        x = __ldcg(reinterpret_cast<const uint4 *>(buf + ((int64_t)p * a.rows + fr) * D) + col);
+                        if (PG != 0 && t0r + row >= cached16) {
+                            if constexpr (PG != 0)
+                                x = __ldcg(reinterpret_cast<const uint4 *>(
+                                               fresh + (int64_t)(first + t0r + row - cached16) * arg.x.kv_stride + h * D) + col);
+                        } else {
+                            const int fr = fp16_row(t0r + row, a.n_sink, a.Ns, a.R, a.head);
+                            x = __ldcg(reinterpret_cast<const uint4 *>(buf + ((int64_t)p * a.rows + fr) * D) + col);
+                        }
                     }
                     *reinterpret_cast<uint4 *>(tst + row * RS + col * 16) = x;
                 }
@@ -1084,7 +1253,7 @@ __global__ void __launch_bounds__(kThreads, 3) decode_split_mma(DecodeArgs a)
                         break;
                     }
                 } else {
-                    stage_rows(a.kr, t0r, n);
+                    stage_rows(a.kr, fresh_rows(arg, 0), t0r, n);
                 }
                 __syncwarp();
                 // scores: K[16 tokens][128] . B.  FP8 keys go straight from the
@@ -1153,16 +1322,38 @@ __global__ void __launch_bounds__(kThreads, 3) decode_split_mma(DecodeArgs a)
                     sc[0][1][0] = cacc[2] * ks;
                     sc[0][1][NH - 1] = cacc[3] * ks;
                 }
+                cap_scores(sc, 1);
     #pragma unroll
                 for (int j = 0; j < NH; ++j) {
-                    if (r >= n)
+                    bool see0 = r < n, see1 = r + 8 < n;
+                    if constexpr (PG != 0) {
+                        // new token t0r + r - cached16 is seen from its own row on
+                        if (!hist && !arg.x.full) {
+                            const int upto = cached16 + (row0 + (GQ == 4 ? t : 2 * t + j)) / arg.c.g - t0r;
+                            see0 = see0 && r <= upto;
+                            see1 = see1 && r + 8 <= upto;
+                        }
+                    }
+                    if (!see0)
                         sc[0][0][j] = -INFINITY;
-                    if (r + 8 >= n)
+                    if (!see1)
                         sc[0][1][j] = -INFINITY;
+                }
+                if constexpr (PG == 2) {
+                    if (hist) {
+                        weigh_unit(sc, 1, (h_lo + (int64_t)tile * RT) / RT);
+                        __syncwarp();                       // the raw tile is fully read
+                        const bool go = lane == 0 && jh + C::STAGES < nhw;
+                        fence_proxy_async_if(go);
+                        issue_tile(jh + C::STAGES, go);
+                        continue;
+                    }
                 }
                 float pr[2][2][NH];
                 float alpha[NH];
                 softmax_step(sc, pr, alpha);                // rescales o_acc (the FP8 history) too
+                if constexpr (PG == 2)
+                    continue;                               // the weights need no values
                 {
                     const float2 al = make_float2(alpha[0], alpha[NH - 1]);
     #pragma unroll
@@ -1180,7 +1371,7 @@ __global__ void __launch_bounds__(kThreads, 3) decode_split_mma(DecodeArgs a)
                     fence_proxy_async_if(go);
                     issue_tile(jh + C::STAGES, go);
                 } else {
-                    stage_rows(a.vr, t0r, n);
+                    stage_rows(a.vr, fresh_rows(arg, 1), t0r, n);
                 }
                 __syncwarp();
                 uint32_t b0, b1;
@@ -1282,7 +1473,7 @@ __global__ void __launch_bounds__(kThreads, 3) decode_split_mma(DecodeArgs a)
             smax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(smax)));
             // |q*s| < 2^(eb + 1) for every entry; scale so that it stays < 2^15
             const float bound = smax * qmax;
-            int E = 14 - (((__float_as_int(bound) >> 23) & 0xff) - 127);
+            int E = 14 + (PG == 2 ? kNormal : 0) - (((__float_as_int(bound) >> 23) & 0xff) - 127);
             E = min(max(E, -100), 100);
             kscale = exp2i(24 - E);
             // v = q s 2^(E - o_k) exactly (power-of-two factors), and
@@ -1421,6 +1612,15 @@ __global__ void __launch_bounds__(kThreads, 3) decode_split_mma(DecodeArgs a)
                             a2 = code_pair_k<4>(wa[kt][q0 + 1], sa[kt][q0 + 1], pos);
                             a3 = code_pair_k<4>(wb[kt][q0 + 1], sb[kt][q0 + 1], pos);
                         }
+                        if constexpr (PG == 2) {
+                            const int o = code_o((BITS == 2) ? 2 * s2 : 4 * (s2 & 3), BITS);
+                            const __half f = __ushort_as_half((unsigned short)((15 + kNormal - o) << 10));
+                            const __half2 ff = __halves2half2(f, f);
+                            a0 = hmul2_u32(a0, ff);
+                            a1 = hmul2_u32(a1, ff);
+                            a2 = hmul2_u32(a2, ff);
+                            a3 = hmul2_u32(a3, ff);
+                        }
                         mma_f16(cacc[kt], a0, a1, a2, a3, bh[2 * ss], bh[2 * ss + 1]);
                         if constexpr (GQ == 8)
                             mma_f16(cacc[kt], a0, a1, a2, a3, bl[2 * ss], bl[2 * ss + 1]);
@@ -1442,6 +1642,10 @@ __global__ void __launch_bounds__(kThreads, 3) decode_split_mma(DecodeArgs a)
             }
         }
 
+        cap_scores(sc, 2);
+        if constexpr (PG == 2) {
+            weigh_unit(sc, 2, wg0 * UG + i);
+        } else {
         // ---- online softmax over the 32 tokens (per warp) -----------------
         float pr[2][2][NH];
         float alpha[NH];
@@ -1465,6 +1669,10 @@ __global__ void __launch_bounds__(kThreads, 3) decode_split_mma(DecodeArgs a)
         constexpr int TOP = 10 - BITS;                  // top of the fp16 mantissa
         constexpr int RL = G / 8;                       // codes per run
         constexpr int NHALF = CH / 2;                   // 16-bit halves per lane chunk
+        // Paged: the zero-point sums take p*s as the mma does, rounded to
+        // fp16.  The rounding then multiplies (code - z) s, the value itself,
+        // and not the code: a value near zero keeps an error of its own size.
+        //
         // B operand (p*s) per k-tile: query group 4 puts value groups j and
         // j + 1 into columns 2 head and 2 head + 1 (one transpose serves two
         // groups), query group 8 one group per transpose with heads 2t, 2t+1
@@ -1503,21 +1711,31 @@ __global__ void __launch_bounds__(kThreads, 3) decode_split_mma(DecodeArgs a)
 #pragma unroll
                 for (int jb = 0; jb < VG / 2; ++jb) {
                     const int j0 = 2 * jb, j1 = 2 * jb + 1;
-                    const float2 pA = __fmul2_rn(prA, make_float2(sA[j0], sA[j1]));
-                    const float2 pB = __fmul2_rn(prB, make_float2(sB[j0], sB[j1]));
+                    float2 pA = __fmul2_rn(prA, make_float2(sA[j0], sA[j1]));
+                    float2 pB = __fmul2_rn(prB, make_float2(sB[j0], sB[j1]));
+                    uint32_t hA, hB;
+                    const float2 rA = round_f16(pA, hA), rB = round_f16(pB, hB);
+                    if constexpr (PG != 0) {     // see "paged" below
+                        pA = rA;
+                        pB = rB;
+                    }
                     float2 z = make_float2(zacc[j0][0], zacc[j1][0]);
                     z = __ffma2_rn(pA, make_float2(zA[j0], zA[j1]),
                                    __ffma2_rn(pB, make_float2(zB[j0], zB[j1]), z));
                     zacc[j0][0] = z.x;
                     zacc[j1][0] = z.y;
-                    bb[kt][jb][0] = movmatrix_t(pack_f16(pA.x, pA.y));
-                    bb[kt][jb][1] = movmatrix_t(pack_f16(pB.x, pB.y));
+                    bb[kt][jb][0] = movmatrix_t(hA);
+                    bb[kt][jb][1] = movmatrix_t(hB);
                 }
             } else if constexpr (GQ == 4) {
                 float pA[VG], pB[VG];
 #pragma unroll
                 for (int j = 0; j < VG; ++j) {
-                    const float2 pAB = __fmul2_rn(make_float2(pr[kt][0][0], pr[kt][1][0]), make_float2(sA[j], sB[j]));
+                    float2 pAB = __fmul2_rn(make_float2(pr[kt][0][0], pr[kt][1][0]), make_float2(sA[j], sB[j]));
+                    if constexpr (PG != 0) {
+                        uint32_t h;
+                        pAB = round_f16(pAB, h);
+                    }
                     pA[j] = pAB.x;
                     pB[j] = pAB.y;
                     zacc[j][0] = fmaf(pAB.x, zA[j], fmaf(pAB.y, zB[j], zacc[j][0]));
@@ -1543,6 +1761,11 @@ __global__ void __launch_bounds__(kThreads, 3) decode_split_mma(DecodeArgs a)
                     for (int hh = 0; hh < NH; ++hh) {
                         pA[hh] = __fmul2_rn(make_float2(pr[kt][0][hh], pr[kt][0][hh]), sA2);
                         pB[hh] = __fmul2_rn(make_float2(pr[kt][1][hh], pr[kt][1][hh]), sB2);
+                        if constexpr (PG != 0) {
+                            uint32_t h;
+                            pA[hh] = round_f16(pA[hh], h);
+                            pB[hh] = round_f16(pB[hh], h);
+                        }
                         float2 z = make_float2(zacc[j0][hh], zacc[j1][hh]);
                         z = __ffma2_rn(pA[hh], zA2, __ffma2_rn(pB[hh], zB2, z));
                         zacc[j0][hh] = z.x;
@@ -1556,8 +1779,13 @@ __global__ void __launch_bounds__(kThreads, 3) decode_split_mma(DecodeArgs a)
             } else {
 #pragma unroll
                 for (int j = 0; j < VG; ++j) {
-                    const float2 pA = __fmul2_rn(make_float2(pr[kt][0][0], pr[kt][0][NH - 1]), make_float2(sA[j], sA[j]));
-                    const float2 pB = __fmul2_rn(make_float2(pr[kt][1][0], pr[kt][1][NH - 1]), make_float2(sB[j], sB[j]));
+                    float2 pA = __fmul2_rn(make_float2(pr[kt][0][0], pr[kt][0][NH - 1]), make_float2(sA[j], sA[j]));
+                    float2 pB = __fmul2_rn(make_float2(pr[kt][1][0], pr[kt][1][NH - 1]), make_float2(sB[j], sB[j]));
+                    if constexpr (PG != 0) {
+                        uint32_t h;
+                        pA = round_f16(pA, h);
+                        pB = round_f16(pB, h);
+                    }
                     float2 z2 = make_float2(zacc[j][0], zacc[j][NH - 1]);
                     z2 = __ffma2_rn(pA, make_float2(zA[j], zA[j]), __ffma2_rn(pB, make_float2(zB[j], zB[j]), z2));
                     zacc[j][0] = z2.x;
@@ -1633,6 +1861,8 @@ __global__ void __launch_bounds__(kThreads, 3) decode_split_mma(DecodeArgs a)
             }
         }
 
+        }
+
         __syncwarp();   // every lane is done with this stage
         {
             const bool go = lane == 0 && i + C::STAGES < nw;
@@ -1644,6 +1874,15 @@ __global__ void __launch_bounds__(kThreads, 3) decode_split_mma(DecodeArgs a)
     if constexpr (!C::TILES_FIRST)
         run_tiles();
     __syncthreads();
+    if (PG == 2 && s_failed) {
+        if (tid < a.g) {
+            for (int k = split; k < (split == a.S - 1 ? a.S + 1 : split + 1); ++k) {
+                a.ws_m[(qrow0 + tid) * (a.S + 1) + k] = -INFINITY;
+                a.ws_l[(qrow0 + tid) * (a.S + 1) + k] = 0.0f;
+            }
+        }
+        return;
+    }
     if (s_failed) {
         // no shared-memory epilogue (a late copy may still land in a stage):
         // empty partials straight from registers; the host reads the status
@@ -1660,7 +1899,9 @@ __global__ void __launch_bounds__(kThreads, 3) decode_split_mma(DecodeArgs a)
     if constexpr (C::TILES_FIRST) {
         if (warp < ntile) {
             // to the final running max: 2^(max when parked - final max)
-            const float2 f = make_float2(ex2_ftz(m_park[0] - m_run[0]), ex2_ftz(m_park[NH - 1] - m_run[NH - 1]));
+            // (paged: a row that saw nothing so far has no output to rescale)
+            const float2 f = make_float2(PG != 0 && m_park[0] == -INFINITY ? 0.0f : ex2_ftz(m_park[0] - m_run[0]),
+                                         PG != 0 && m_park[NH - 1] == -INFINITY ? 0.0f : ex2_ftz(m_park[NH - 1] - m_run[NH - 1]));
 #pragma unroll
             for (int i = 0; i < 4 * NO; ++i) {
                 const float4 v = ores_park[32 * i];
@@ -1690,6 +1931,36 @@ __global__ void __launch_bounds__(kThreads, 3) decode_split_mma(DecodeArgs a)
         for (int s = 0; s < C::STAGES; ++s)
             mbar_inval(bar0 + 8 * s);
     __syncthreads();   // every warp has left its pipeline; its memory is free
+    if constexpr (PG == 2) {
+        float *mw = reinterpret_cast<float *>(smem), *lw = mw + C::NWARP * GQ;
+        if (r == 0) {
+#pragma unroll
+            for (int jj = 0; jj < NH; ++jj) {
+                const int hh = (GQ == 4) ? t : 2 * t + jj;
+                mw[warp * GQ + hh] = m_run[jj];
+                lw[warp * GQ + hh] = l_w[jj];
+            }
+        }
+        __syncthreads();
+        if (tid < a.g) {
+            float M = -INFINITY, L = 0.0f;
+#pragma unroll
+            for (int w = 0; w < C::NWARP; ++w)
+                M = fmaxf(M, mw[w * GQ + tid]);
+#pragma unroll
+            for (int w = 0; w < C::NWARP; ++w)
+                if (lw[w * GQ + tid] > 0.0f)
+                    L = fmaf(lw[w * GQ + tid], exp2f(mw[w * GQ + tid] - M), L);
+            const int64_t idx = (qrow0 + tid) * (a.S + 1) + split;
+            a.ws_m[idx] = M;
+            a.ws_l[idx] = L;
+            if (split == a.S - 1) {
+                a.ws_m[idx + 1] = -INFINITY;
+                a.ws_l[idx + 1] = 0.0f;
+            }
+        }
+        return;
+    }
     float *om = reinterpret_cast<float *>(smem);                 // [4 warps][GQ][D]
     float *mw = om + C::NWARP * GQ * D;                          // [4][GQ]
     float *lw = mw + C::NWARP * GQ;                              // [4][GQ]
@@ -1828,6 +2099,43 @@ cudaError_t launch_mma(const DecodeArgs &a, int pairs, cudaStream_t s, int *bloc
     dim3 grid((unsigned)a.S, (unsigned)pairs);
     kernel<<<grid, kThreads, C::SMEM, s>>>(a);
     return cudaGetLastError();
+}
+
+// The paged forms (kivi_paged_decode.cuh).
+template <int BITS, int G, int GQ, int MF, int F8, int PG>
+cudaError_t launch_paged_mma(const PagedDecodeArgs &a, int pairs, cudaStream_t s, int *blocks_per_sm)
+{
+    using C = MmaCfg<BITS, G, GQ, MF, F8>;
+    auto kernel = decode_split_mma<BITS, G, GQ, MF, F8, PG>;
+    static std::atomic<uint64_t> prepared{0};
+    cudaError_t e = prepare_on_device(kernel, C::SMEM, prepared);
+    if (e != cudaSuccess)
+        return e;
+    if (blocks_per_sm)
+        return cudaOccupancyMaxActiveBlocksPerMultiprocessor(blocks_per_sm, kernel, kThreads, C::SMEM);
+    kernel<<<dim3((unsigned)a.d.S, (unsigned)pairs, (unsigned)((a.rows + GQ - 1) / GQ)), kThreads, C::SMEM, s>>>(a);
+    return cudaGetLastError();
+}
+
+template <int BITS, int G, int MF, int F8>
+cudaError_t launch_paged_g(const PagedDecodeArgs &a, int gq, bool weights, int pairs, cudaStream_t s, int *bps)
+{
+    if (gq == 4)
+        return weights ? launch_paged_mma<BITS, G, 4, MF, F8, 2>(a, pairs, s, bps)
+                       : launch_paged_mma<BITS, G, 4, MF, F8, 1>(a, pairs, s, bps);
+    return weights ? launch_paged_mma<BITS, G, 8, MF, F8, 2>(a, pairs, s, bps)
+                   : launch_paged_mma<BITS, G, 8, MF, F8, 1>(a, pairs, s, bps);
+}
+
+template <int BITS, int MF>
+cudaError_t launch_paged_bits(const PagedDecodeArgs &a, int gq, bool weights, int pairs, cudaStream_t s, int *bps)
+{
+    switch (a.c.G) {
+    case 32: return launch_paged_g<BITS, 32, MF, 0>(a, gq, weights, pairs, s, bps);
+    case 64: return launch_paged_g<BITS, 64, MF, 0>(a, gq, weights, pairs, s, bps);
+    case 128: return launch_paged_g<BITS, 128, MF, 0>(a, gq, weights, pairs, s, bps);
+    default: return cudaErrorInvalidValue;
+    }
 }
 
 template <int BITS, int G, int MAXG, int MF>

@@ -114,6 +114,19 @@ cudaError_t launch_paged_weights(const PagedArgs &c, const ChunkArgs &x, float *
 cudaError_t launch_paged_evict(const PagedArgs &c, float *weights, int budget, int recent, void *ws,
                                cudaStream_t s, int *launches);
 
+// Partial results of the splits: part i of query row r of pair p (the p-th of
+// the launch) at index (p rows + r) parts + i, its maximum (log2 units) and sum
+// at m, l [index step], its unnormalised output at o[index D].
+struct Parts {
+    const float *m, *l, *o;
+    int step, parts;
+    int pair0;                // first pair of the launch
+    int row0, rows;           // first query row of the launch, and rows a pair has room for
+};
+
+// Joins the parts of launched pairs into out: a warp per query row.
+cudaError_t launch_join(const PagedArgs &c, const ChunkArgs &x, const Parts &d, __half *out, int pairs, cudaStream_t s);
+
 // The attention of long chunks (kivi_paged_tc.cu).
 bool is_long_chunk(const PagedArgs &c, int max_new);
 size_t long_chunk_bytes(const PagedArgs &c, int max_new, int max_cached);

@@ -13,6 +13,7 @@
 #include <algorithm>
 
 #include "kivi_paged_attend.cuh"
+#include "kivi_paged_decode.cuh"
 
 namespace kivi {
 namespace {
@@ -281,10 +282,10 @@ __global__ void __launch_bounds__(kAttendThreads) attend_kernel(PagedArgs c, Chu
 }
 
 // Joins the splits of the attention: a warp per query row, four channels a lane.
-__global__ void __launch_bounds__(128) join_kernel(PagedArgs c, ChunkArgs x, SplitOut d)
+__global__ void __launch_bounds__(128) join_kernel(PagedArgs c, ChunkArgs x, Parts d, __half *out)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int p = blockIdx.y, b = p / c.Hkv, h = p % c.Hkv;
+    const int p = d.pair0 + blockIdx.y, b = p / c.Hkv, h = p % c.Hkv;
     int first, T;
     PagedState st;
     if (!sequence(c, x, b, first, T, st))
@@ -293,30 +294,31 @@ __global__ void __launch_bounds__(128) join_kernel(PagedArgs c, ChunkArgs x, Spl
     if (row >= T * c.g)
         return;
     const int64_t at = (int64_t)(first + row / c.g) * (c.Hkv * c.g) + h * c.g + row % c.g;
-    const int64_t part = ((int64_t)p * d.rows + row) * d.S;
+    const int64_t part = ((int64_t)blockIdx.y * d.rows + row) * d.parts;
     float M = -INFINITY, L = 0.0f;
     float4 O = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int i = 0; i < d.S; ++i)
-        M = fmaxf(M, d.ml[part + i].x);
-    for (int i = 0; i < d.S; ++i) {
-        const float2 ml = d.ml[part + i];
-        if (!(ml.y > 0.0f))
+    for (int i = 0; i < d.parts; ++i)
+        M = fmaxf(M, d.m[(part + i) * d.step]);
+    for (int i = 0; i < d.parts; ++i) {
+        const float l = d.l[(part + i) * d.step];
+        if (!(l > 0.0f))
             continue;
-        const float w = ex2(ml.x - M);
+        const float w = ex2(d.m[(part + i) * d.step] - M);
         const float4 v = *reinterpret_cast<const float4 *>(d.o + (part + i) * kHeadDim + 4 * lane);
-        L = fmaf(ml.y, w, L);
+        L = fmaf(l, w, L);
         O.x = fmaf(v.x, w, O.x);
         O.y = fmaf(v.y, w, O.y);
         O.z = fmaf(v.z, w, O.z);
         O.w = fmaf(v.w, w, O.w);
     }
     const float inv = L > 0.0f ? 1.0f / L : 0.0f;
-    *reinterpret_cast<uint2 *>(d.out + at * kHeadDim + 4 * lane) =
+    *reinterpret_cast<uint2 *>(out + at * kHeadDim + 4 * lane) =
         make_uint2(pack_sat(O.x * inv, O.y * inv), pack_sat(O.z * inv, O.w * inv));
 }
 
 // Adds a page's share of every row: a thread per page, the rows in order.
-__global__ void __launch_bounds__(128) weigh_kernel(PagedArgs c, ChunkArgs x, SplitOut d, float *weights)
+__global__ void __launch_bounds__(128) weigh_kernel(PagedArgs c, ChunkArgs x, Parts d, const float *page_sums,
+                                                    int unit, int units, float *weights)
 {
     __shared__ float lse[128];
     const int p = blockIdx.y, b = p / c.Hkv;
@@ -328,24 +330,26 @@ __global__ void __launch_bounds__(128) weigh_kernel(PagedArgs c, ChunkArgs x, Sp
     const int col = blockIdx.x * 128 + threadIdx.x;
     if (blockIdx.x * 128 >= st.held || rows <= 0)
         return;
-    const int per = c.G / d.unit;
+    const int per = c.G / unit;
     float sum = 0.0f;
     for (int r0 = 0; r0 < rows; r0 += 128) {
         __syncthreads();
         if (r0 + threadIdx.x < rows) {
-            const float2 *ml = d.ml + ((int64_t)p * d.rows + r0 + threadIdx.x) * d.S;
+            const int64_t part = ((int64_t)p * d.rows + r0 + threadIdx.x) * d.parts;
             float M = -INFINITY, L = 0.0f;
-            for (int i = 0; i < d.S; ++i)
-                M = fmaxf(M, ml[i].x);
-            for (int i = 0; i < d.S; ++i)
-                if (ml[i].y > 0.0f)
-                    L = fmaf(ml[i].y, ex2(ml[i].x - M), L);
+            for (int i = 0; i < d.parts; ++i)
+                M = fmaxf(M, d.m[(part + i) * d.step]);
+            for (int i = 0; i < d.parts; ++i) {
+                const float l = d.l[(part + i) * d.step];
+                if (l > 0.0f)
+                    L = fmaf(l, ex2(d.m[(part + i) * d.step] - M), L);
+            }
             lse[threadIdx.x] = M + log2f(L);
         }
         __syncthreads();
         if (col < st.held)
             for (int r = 0; r < min(128, rows - r0); ++r) {
-                const float *ls = d.ls + ((int64_t)p * d.rows + r0 + r) * d.units + col * per;
+                const float *ls = page_sums + ((int64_t)p * d.rows + r0 + r) * units + (int64_t)col * per;
                 for (int k = 0; k < per; ++k)
                     sum += ex2(ls[k] - lse[r]);
             }
@@ -381,9 +385,15 @@ int split_count(int64_t blocks, int max_new, int max_cached)
 
 constexpr int64_t kWeighBytes = 256ll << 20;     // rows of page sums held at once
 
-}  // namespace
+// ------------------------------------------------------------------- plans ---
+// Few query rows per pair: the decode kernel (kivi_paged_decode.cuh), which
+// streams the packed codes into the matrix instructions.  It takes 4 or 8 rows
+// and reads the pages again for the next 8.  Groups of 16 tokens it does not
+// know.
+constexpr int kFewRows = 8;
+constexpr int kDecodeBlocks = 4096;              // (pair, row tile, split) blocks of it that the workspace is sized for
 
-namespace {
+bool few_rows(const PagedArgs &c, int max_new) { return c.G >= 32 && (int64_t)max_new * c.g <= kFewRows; }
 
 struct Plan {
     int splits;           // parts of a pair's tokens
@@ -412,14 +422,107 @@ Plan weights_plan(const PagedArgs &c, int max_new, int max_cached)
     return p;
 }
 
+cudaError_t paged_decode(const PagedDecodeArgs &a, bool weights, int pairs, cudaStream_t s, int *blocks_per_sm)
+{
+    const int gq = a.rows <= 4 ? 4 : 8;
+    if (a.c.fmt)
+        return launch_paged_decode_fp8(a, gq, weights, pairs, s, blocks_per_sm);
+    if (a.c.bits == 2)
+        return a.c.meta ? launch_paged_decode_2_f16(a, gq, weights, pairs, s, blocks_per_sm)
+                        : launch_paged_decode_2(a, gq, weights, pairs, s, blocks_per_sm);
+    return a.c.meta ? launch_paged_decode_4_f16(a, gq, weights, pairs, s, blocks_per_sm)
+                    : launch_paged_decode_4(a, gq, weights, pairs, s, blocks_per_sm);
+}
+
+// Query rows the partial results of a decode launch have room for.
+int few_room(const PagedArgs &c, int max_new)
+{
+    const int rows = max_new * c.g;
+    return rows <= 4 ? 4 : (rows + 7) / 8 * 8;
+}
+
+// Splits of a decode launch: the count with the smallest waves x (fixed cost +
+// chunks per block) for the blocks the GPU holds at once -- the cost model of
+// kivi_decode_num_splits, for the longest sequence the bounds allow.
+cudaError_t few_splits(const PagedDecodeArgs &a, bool weights, int64_t blocks, int max_cached, int *splits)
+{
+    int dev = 0, sms = 0, per_sm = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess)
+        e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess)
+        e = paged_decode(a, weights, 0, nullptr, &per_sm);
+    if (e != cudaSuccess)
+        return e;
+    const int64_t resident = (int64_t)std::max(per_sm, 1) * sms;
+    const int64_t chunks = std::max<int64_t>(1, ((int64_t)max_cached + kChunk - 1) / kChunk);
+    const int64_t most = std::max<int64_t>(1, std::min<int64_t>(kDecodeBlocks / blocks, chunks));
+    int64_t best = INT64_MAX;
+    *splits = 1;
+    for (int64_t k = 1; k <= most; ++k) {
+        const int64_t cost = (blocks * k + resident - 1) / resident * (12 + (chunks + k - 1) / k);
+        if (cost < best) {
+            best = cost;
+            *splits = (int)k;
+        }
+    }
+    return cudaSuccess;
+}
+
+PagedDecodeArgs decode_args_of(const PagedArgs &c, const ChunkArgs &x, int rows)
+{
+    PagedDecodeArgs a{};
+    a.c = c;
+    a.x = x;
+    a.rows = rows;
+    a.cap_log2_inv = x.cap_log2 != 0.0f ? 1.0f / x.cap_log2 : 0.0f;
+    a.d.kr = c.k_fp16;
+    a.d.vr = c.v_fp16;
+    a.d.status = c.control;
+    a.d.Ns = c.Ns;
+    a.d.R = c.R;
+    a.d.rows = c.rows;
+    a.d.Hkv = c.Hkv;
+    a.d.scale_log2 = x.scale_log2;
+    a.d.fp8_k_scale = c.fp8_k_scale;
+    a.d.fp8_v_scale = c.fp8_v_scale;
+    return a;
+}
+
+// Partial results of a decode launch in the workspace: o (attention), m, l.
+size_t few_parts(PagedDecodeArgs &a, int64_t pairs, bool weights, void *ws)
+{
+    const int64_t n = pairs * a.rows * (a.d.S + 1);
+    a.d.ws_o = static_cast<float *>(ws);
+    a.d.ws_m = a.d.ws_o + (weights ? 0 : n * kHeadDim);
+    a.d.ws_l = a.d.ws_m + n;
+    return (size_t)n * ((weights ? 0 : kHeadDim) + 2) * 4;
+}
+
+// splits * blocks <= max(kDecodeBlocks, blocks), and one more part per row
+size_t few_bytes(const PagedArgs &c, int max_new, bool weights)
+{
+    const int rows = few_room(c, max_new), gq = rows <= 4 ? 4 : 8;
+    const int64_t blocks = (int64_t)c.B * c.Hkv * (rows / gq);
+    return (size_t)(std::max<int64_t>(kDecodeBlocks, blocks) + blocks) * gq * ((weights ? 0 : kHeadDim) + 2) * 4;
+}
+
 }  // namespace
+
+cudaError_t launch_join(const PagedArgs &c, const ChunkArgs &x, const Parts &d, __half *out, int pairs, cudaStream_t s)
+{
+    join_kernel<<<dim3((unsigned)(((int64_t)x.max_new * c.g + 3) / 4), pairs), 128, 0, s>>>(c, x, d, out);
+    return cudaGetLastError();
+}
 
 size_t attention_bytes(const PagedArgs &c, int max_new, int max_cached)
 {
     // splits * blocks < blocks + target, and more blocks than that mean one split
     const int64_t blocks = std::min<int64_t>((int64_t)c.B * c.Hkv * attend_plan(c, max_new, max_cached).row_tiles,
                                              kTargetBlocks);
-    return (size_t)(kTile * (blocks + kTargetBlocks)) * (kHeadDim + 2) * 4;
+    const size_t tiles = (size_t)(kTile * (blocks + kTargetBlocks)) * (kHeadDim + 2) * 4;
+    const int few = std::min(max_new, std::max(1, kFewRows / c.g));       // the longest chunk of few rows
+    return std::max(tiles, few_bytes(c, few, false));
 }
 
 size_t weights_bytes(const PagedArgs &c, int max_new, int max_cached)
@@ -427,7 +530,10 @@ size_t weights_bytes(const PagedArgs &c, int max_new, int max_cached)
     const int64_t pairs = (int64_t)c.B * c.Hkv;
     const int64_t units = (int64_t)c.columns * c.G / weigh_unit(c);
     const int64_t tiles = pairs * weights_plan(c, max_new, max_cached).row_tiles;
-    return (size_t)tiles * kTile * units * 4 + (size_t)kTile * (tiles + kTargetBlocks) * 8;
+    const size_t all = (size_t)tiles * kTile * units * 4 + (size_t)kTile * (tiles + kTargetBlocks) * 8;
+    const int few = std::min(max_new, std::max(1, kFewRows / c.g));
+    const size_t sums = (size_t)pairs * few_room(c, few) * ((size_t)c.columns * c.G / decode_unit(c)) * 4;
+    return std::max(all, few_bytes(c, few, true) + sums);
 }
 
 cudaError_t launch_paged_attention(const PagedArgs &c, const ChunkArgs &x, __half *out, void *ws, cudaStream_t s,
@@ -435,8 +541,21 @@ cudaError_t launch_paged_attention(const PagedArgs &c, const ChunkArgs &x, __hal
 {
     if (is_long_chunk(c, x.max_new))
         return launch_long_chunk(c, x, out, ws, s, launches);
-    const Plan p = attend_plan(c, x.max_new, x.max_cached);
     const int pairs = c.B * c.Hkv;
+    if (few_rows(c, x.max_new)) {
+        PagedDecodeArgs a = decode_args_of(c, x, few_room(c, x.max_new));
+        const int64_t blocks = (int64_t)pairs * (a.rows <= 4 ? 1 : a.rows / 8);
+        cudaError_t e = few_splits(a, false, blocks, x.max_cached, &a.d.S);
+        if (e != cudaSuccess)
+            return e;
+        few_parts(a, pairs, false, ws);
+        e = paged_decode(a, false, pairs, s, nullptr);
+        if (e != cudaSuccess)
+            return e;
+        *launches = 2;
+        return launch_join(c, x, Parts{a.d.ws_m, a.d.ws_l, a.d.ws_o, 1, a.d.S + 1, 0, 0, a.rows}, out, pairs, s);
+    }
+    const Plan p = attend_plan(c, x.max_new, x.max_cached);
     SplitOut d{};
     d.out = out;
     d.S = p.splits;
@@ -445,19 +564,37 @@ cudaError_t launch_paged_attention(const PagedArgs &c, const ChunkArgs &x, __hal
     d.ml = reinterpret_cast<float2 *>(d.o + (int64_t)pairs * d.rows * p.splits * kHeadDim);
     launch_attend<false>(c, x, d, dim3(p.splits, pairs, p.row_tiles), s);
     *launches = 1;
-    cudaError_t e = cudaGetLastError();
+    const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || p.splits == 1)
         return e;
-    join_kernel<<<dim3((unsigned)(((int64_t)x.max_new * c.g + 3) / 4), pairs), 128, 0, s>>>(c, x, d);
     *launches = 2;
-    return cudaGetLastError();
+    const float *ml = reinterpret_cast<const float *>(d.ml);
+    return launch_join(c, x, Parts{ml, ml + 1, d.o, 2, p.splits, 0, 0, d.rows}, out, pairs, s);
 }
 
 cudaError_t launch_paged_weights(const PagedArgs &c, const ChunkArgs &x, float *weights, void *ws, cudaStream_t s,
                                  int *launches)
 {
-    const Plan p = weights_plan(c, x.max_new, x.max_cached);
     const int pairs = c.B * c.Hkv;
+    const dim3 grid((c.columns + 127) / 128, pairs);
+    if (few_rows(c, x.max_new)) {
+        PagedDecodeArgs a = decode_args_of(c, x, few_room(c, x.max_new));
+        const int64_t blocks = (int64_t)pairs * (a.rows <= 4 ? 1 : a.rows / 8);
+        cudaError_t e = few_splits(a, true, blocks, x.max_cached, &a.d.S);
+        if (e != cudaSuccess)
+            return e;
+        const int unit = decode_unit(c);
+        a.units = c.columns * c.G / unit;
+        a.ls = reinterpret_cast<float *>(static_cast<char *>(ws) + few_parts(a, pairs, true, ws));
+        e = paged_decode(a, true, pairs, s, nullptr);
+        if (e != cudaSuccess)
+            return e;
+        weigh_kernel<<<grid, 128, 0, s>>>(c, x, Parts{a.d.ws_m, a.d.ws_l, nullptr, 1, a.d.S + 1, 0, 0, a.rows}, a.ls,
+                                          unit, a.units, weights);
+        *launches = 2;
+        return cudaGetLastError();
+    }
+    const Plan p = weights_plan(c, x.max_new, x.max_cached);
     SplitOut d{};
     d.S = p.splits;
     d.unit = weigh_unit(c);
@@ -465,11 +602,13 @@ cudaError_t launch_paged_weights(const PagedArgs &c, const ChunkArgs &x, float *
     d.rows = p.row_tiles * kTile;
     d.ls = static_cast<float *>(ws);
     d.ml = reinterpret_cast<float2 *>(d.ls + (int64_t)pairs * d.rows * d.units);
+    const float *ml = reinterpret_cast<const float *>(d.ml);
     *launches = 0;
     for (int64_t r0 = 0; r0 < (int64_t)x.max_new * c.g; r0 += d.rows) {
         d.row0 = (int)r0;
         launch_attend<true>(c, x, d, dim3(p.splits, pairs, p.row_tiles), s);
-        weigh_kernel<<<dim3((c.columns + 127) / 128, pairs), 128, 0, s>>>(c, x, d, weights);
+        weigh_kernel<<<grid, 128, 0, s>>>(c, x, Parts{ml, ml + 1, nullptr, 2, p.splits, 0, d.row0, d.rows}, d.ls, d.unit,
+                                          d.units, weights);
         *launches += 2;
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess)

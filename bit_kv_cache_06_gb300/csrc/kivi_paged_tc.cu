@@ -511,41 +511,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(PagedArgs c, ChunkArg
     }
 }
 
-// Joins the splits: a warp per query row, four channels a lane.
-__global__ void __launch_bounds__(128) tc_join_kernel(PagedArgs c, ChunkArgs x, TcOut d)
-{
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int p = d.pair0 + blockIdx.y, b = p / c.Hkv, h = p % c.Hkv;
-    int first, T;
-    PagedState st;
-    if (!sequence(c, x, b, first, T, st))
-        return;
-    const int row = blockIdx.x * 4 + warp;
-    if (row >= T * c.g)
-        return;
-    const int64_t at = (int64_t)(first + row / c.g) * (c.Hkv * c.g) + h * c.g + row % c.g;
-    const int64_t part = ((int64_t)blockIdx.y * d.rows + row) * d.S;
-    float M = -INFINITY, L = 0.0f;
-    float4 O = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int i = 0; i < d.S; ++i)
-        M = fmaxf(M, d.ml[part + i].x);
-    for (int i = 0; i < d.S; ++i) {
-        const float2 ml = d.ml[part + i];
-        if (!(ml.y > 0.0f))
-            continue;
-        const float w = ex2(ml.x - M);
-        const float4 v = *reinterpret_cast<const float4 *>(d.o + (part + i) * kHeadDim + 4 * lane);
-        L = fmaf(ml.y, w, L);
-        O.x = fmaf(v.x, w, O.x);
-        O.y = fmaf(v.y, w, O.y);
-        O.z = fmaf(v.z, w, O.z);
-        O.w = fmaf(v.w, w, O.w);
-    }
-    const float inv = L > 0.0f ? 1.0f / L : 0.0f;
-    *reinterpret_cast<uint2 *>(d.out + at * kHeadDim + 4 * lane) =
-        make_uint2(pack_sat(O.x * inv, O.y * inv), pack_sat(O.z * inv, O.w * inv));
-}
-
 constexpr int kTcSmem = sizeof(TcSmem) + 1024;
 constexpr int kTcBlocks = 152;
 
@@ -625,7 +590,10 @@ cudaError_t launch_long_chunk(const PagedArgs &c, const ChunkArgs &x, __half *ou
             tc_kernel<false><<<tgrid, kTcThreads, kTcSmem, s>>>(c, x, d);
         *launches += 2;
         if (p.splits > 1) {
-            tc_join_kernel<<<dim3((unsigned)(((int64_t)x.max_new * c.g + 3) / 4), pairs), 128, 0, s>>>(c, x, d);
+            const float *ml = reinterpret_cast<const float *>(d.ml);
+            e = launch_join(c, x, Parts{ml, ml + 1, d.o, 2, p.splits, p0, 0, d.rows}, out, pairs, s);
+            if (e != cudaSuccess)
+                return e;
             *launches += 1;
         }
         e = cudaGetLastError();

@@ -139,7 +139,11 @@ class Model:
         what a rounding is off there whatever the number's size: once for the
         output, once for each value (times its p, which sum to 1), and once
         for each 2^(s_j - m) it multiplies, the divisor being 1 or more: that
-        adds 2^-25 (2 + sum_j |v_j|) over the tokens a row sees."""
+        adds 2^-25 (2 + sum_j |v_j|) over the tokens a row sees.
+        Few query rows: o = sum p s code - sum p s z, two fp32 sums of up to 64
+        slices each (64 steps of 2^-24) whose terms are at most 4 max_c |v_jc|
+        in size (a group's codes span its range, at most twice its largest
+        value; so do z s): 2^-18 sum_j p_j 4 max_c |v_jc|."""
         out = torch.zeros((self.off[-1], self.g * self.Hkv, D), dtype=torch.float64)
         tol = torch.zeros_like(out)
         for b in range(self.B):
@@ -155,7 +159,7 @@ class Model:
                     sl = slice(self.off[b], self.off[b + 1])
                     out[sl, i] = o
                     seen = (p > 0).double()
-                    tol[sl, i] = (2.0 ** -25 * (2 + seen @ V.abs()) + HALF * o.abs() + (2 * HALF + 2.0 ** -14) * (p @ V.abs()) + dp @ V.abs() +
+                    tol[sl, i] = (2.0 ** -16 * (p @ V.abs().amax(1, keepdim=True)) + 2.0 ** -25 * (2 + seen @ V.abs()) + HALF * o.abs() + (2 * HALF + 2.0 ** -14) * (p @ V.abs()) + dp @ V.abs() +
                                   dp.sum(1, keepdim=True) * o.abs())
         return out, tol
 

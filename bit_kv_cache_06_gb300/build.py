@@ -22,7 +22,8 @@ SOURCES = ["kivi_api.cu", "kivi_quant.cu", "kivi_decode.cu", "kivi_decode_f16.cu
            "kivi_decode_fp8.cu", "kivi_paged_api.cu", "kivi_paged_attend.cu",
            "kivi_paged_evict.cu", "kivi_paged_tc.cu", "kivi_paged_decode_2.cu",
            "kivi_paged_decode_2_f16.cu", "kivi_paged_decode_4.cu", "kivi_paged_decode_4_f16.cu",
-           "kivi_paged_decode_fp8.cu"]
+           "kivi_paged_decode_fp8.cu", "kivi_paged_stage_2.cu", "kivi_paged_stage_4.cu",
+           "kivi_paged_stage_fp8.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
               "-I", INCLUDE, "-I", CSRC]

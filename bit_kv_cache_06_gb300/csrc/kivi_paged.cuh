@@ -127,10 +127,17 @@ struct Parts {
 // Joins the parts of launched pairs into out: a warp per query row.
 cudaError_t launch_join(const PagedArgs &c, const ChunkArgs &x, const Parts &d, __half *out, int pairs, cudaStream_t s);
 
-// The attention of long chunks (kivi_paged_tc.cu).
-bool is_long_chunk(const PagedArgs &c, int max_new);
-size_t long_chunk_bytes(const PagedArgs &c, int max_new, int max_cached);
-cudaError_t launch_long_chunk(const PagedArgs &c, const ChunkArgs &x, __half *out, void *ws, cudaStream_t s,
-                              int *launches);
+// Adds the pages' sums of launched pairs to weights: ls[(p rows + r) units + u]
+// holds log2 of the softmax sum of unit u (`unit` tokens) of row r.
+cudaError_t launch_weigh(const PagedArgs &c, const ChunkArgs &x, const Parts &d, const float *ls, int unit, int units,
+                         float *weights, int pairs, cudaStream_t s);
+
+// Many query rows (kivi_paged_tc.cu).
+size_t long_attention_bytes(const PagedArgs &c, int max_new, int max_cached);
+size_t long_weights_bytes(const PagedArgs &c, int max_new, int max_cached);
+cudaError_t launch_long_attention(const PagedArgs &c, const ChunkArgs &x, __half *out, void *ws, cudaStream_t s,
+                                  int *launches);
+cudaError_t launch_long_weights(const PagedArgs &c, const ChunkArgs &x, float *weights, void *ws, cudaStream_t s,
+                                int *launches);
 
 }  // namespace kivi

@@ -152,7 +152,6 @@ size_t workspace_bytes(const PagedArgs &a, int max_new, int max_cached)
         const int most = cached_bound(a, max_cached);
         n = std::max(n, attention_bytes(a, max_new, most));
         n = std::max(n, weights_bytes(a, max_new, most));
-        n = std::max(n, long_chunk_bytes(a, max_new, most));
     }
     return (n + 255) / 256 * 256;
 }

@@ -1,119 +1,47 @@
-// kivi_paged_tc.cu -- attention of long chunks over a paged cache on the
-// 5th-generation tensor cores.
+// kivi_paged_tc.cu -- attention of many query rows over a paged cache, and the
+// softmax weights its pages get, on the 5th-generation tensor cores.
 //
-// A chunk of many new tokens reads every cached token many times (once per 256
-// query rows), so the pages are dequantised once, into the workspace, as the
-// very images the matrix instructions take from shared memory, and the
-// attention itself is a dense one:
+// Every cached token is read once per 256 query rows, so the pages are
+// dequantised once, into the workspace, as the very tiles the matrix
+// instructions take from shared memory (kivi_paged_stage.cuh); what runs here is
+// a dense attention over them.
 //
-//  stage_kernel   a pair's tokens in order (pages, sink, window, new tokens),
-//                 128 to a tile: the keys as [token][channel], the values
-//                 transposed as [channel][token], fp16, each as two panels of
-//                 128-byte rows in the 128-byte swizzle (16-byte chunk i of row
-//                 r lies at chunk i ^ (r & 7)).  Both operands are then K-major.
-//  tc_kernel      256 query rows (two M tiles of 128) of one pair against a
-//                 range of its tiles.  Ten warps: one fetches tiles (a bulk copy
-//                 of 32 KB per operand, two stages), one issues the matrix
-//                 instructions, and a warpgroup per M tile keeps the softmax,
-//                 a thread per query row.  S = Q K^T and O += P V accumulate
-//                 in tensor memory; P (fp16) overwrites the S it came from, so
-//                 one M tile's softmax runs while the other's products do.
-//                 O is only rescaled when a row's maximum has grown by more
-//                 than 2^8 since the last time: until then 2^(s - m) stays
-//                 within fp16 and nothing is lost by an old m.
+//  tc_kernel        256 query rows (two M tiles of 128) of one pair against a
+//                   range of its tiles.  18 warps: one fetches tiles (bulk
+//                   copies, two stages per operand), one issues the matrix
+//                   instructions, and two warpgroups per M tile (a team) keep
+//                   the softmax: a thread has half the columns of one query row.
+//                   S = Q K^T and O += P V accumulate in tensor memory; P (fp16)
+//                   overwrites the S it came from, so one team's softmax runs
+//                   while the other's products do.  Up to 128 rows there is one M
+//                   tile: the teams then take its even and its odd token tiles
+//                   and join at the end.
+//                   O is only rescaled when a row's maximum has grown by more
+//                   than 2^8 since the last time: until then 2^(s - m) stays
+//                   within fp16 and nothing is lost by an old m.
+//  tc_weigh_kernel  the same without values: every step's S is a tensor-memory
+//                   buffer of its own (four in turn), keys have a full low part,
+//                   and a thread turns its row's 128 scores into page sums.
 #include <algorithm>
+#include <type_traits>
 
 #include "kivi_paged_attend.cuh"
+#include "kivi_paged_tc.cuh"
 
 namespace kivi {
 namespace {
 
-constexpr int kTok = 128;                        // tokens per tile
 constexpr int kMTile = 128;                      // query rows per M tile
 constexpr int kRows = 2 * kMTile;                // query rows per block
-constexpr int kImage = kTok * kHeadDim * 2;      // bytes of one operand's tile
-constexpr int kTileBytes = 2 * kImage;           // keys, then values
 constexpr int kStages = 2;
-constexpr int kTcThreads = 320;
-constexpr int kStageThreads = 256;
-constexpr int kLongRows = 128;                   // query rows per pair from which this path is taken
+constexpr int kTcThreads = 576;              // attention: 16 softmax warps, MMA, fetch
+constexpr int kWeighThreads = 320;           // weights: 8, MMA, fetch
+constexpr int kTcBlocks = 152;                   // blocks the GPU holds at once
+constexpr int kPartBlocks = 4 * kTcBlocks;       // blocks of several splits, at most
 constexpr int64_t kStageBytes = 1ll << 30;       // staged pairs per launch
+constexpr int64_t kSumBytes = 256ll << 20;       // page sums held at once
 constexpr long long kWaitCycles = 1ll << 32;     // about 2 s
 constexpr float kRescale = 8.0f;                 // log2 of how far a maximum may run ahead
-
-// ------------------------------------------------------------------ stage ---
-
-struct StageArgs {
-    uint8_t *tiles;           // [pairs of this launch][tiles][kTileBytes]
-    int tiles_per_pair;
-    int pair0;
-};
-
-// 16-byte chunk `chunk` (8 elements) of row r of an image.
-__device__ __forceinline__ int image_at(int r, int chunk)
-{
-    return (chunk >> 3) * (kImage / 2) + r * 128 + (((chunk & 7) ^ (r & 7)) << 4);
-}
-
-template <class F>
-__global__ void __launch_bounds__(kStageThreads) stage_kernel(PagedArgs c, ChunkArgs x, StageArgs a)
-{
-    constexpr int D = kHeadDim, VS = D + 8;
-    __shared__ __align__(16) __half sv[kTok * VS];
-    const int p = a.pair0 + blockIdx.y, b = p / c.Hkv, h = p % c.Hkv, tid = threadIdx.x;
-    int first, T;
-    PagedState st;
-    if (!sequence(c, x, b, first, T, st))
-        return;
-    const int deep = st.held * c.G, cached = deep + st.sink + st.window;
-    const int total = cached + (x.k ? T : 0), base = blockIdx.x * kTok;
-    if (base >= total || T == 0)
-        return;
-    const RecGeo<F> geo(c.G);
-    uint8_t *tile = a.tiles + ((int64_t)blockIdx.y * a.tiles_per_pair + blockIdx.x) * kTileBytes;
-    for (int i = tid; i < kTok * 16; i += kStageThreads) {
-        const int t = i >> 4, c8 = i & 15, u = base + t;
-        uint4 kv = make_uint4(0u, 0u, 0u, 0u), vv = kv;      // tokens behind the last one count as zero
-        if (u < deep) {
-            const unsigned char *rec = page_record(c, p, u / c.G);
-            if (rec) {
-                float f[8];
-                page_k8<F>(rec, geo, u % c.G, c8, c.fp8_k_scale, f);
-                kv = make_uint4(pack_sat(f[0], f[1]), pack_sat(f[2], f[3]), pack_sat(f[4], f[5]), pack_sat(f[6], f[7]));
-                page_v8<F>(rec, geo, u % c.G, c8, c.fp8_v_scale, f);
-                vv = make_uint4(pack_sat(f[0], f[1]), pack_sat(f[2], f[3]), pack_sat(f[4], f[5]), pack_sat(f[6], f[7]));
-            } else if (c8 == 0) {
-                atomicOr(c.control, KIVI_STATUS_BAD_PAGE);
-            }
-        } else if (u < total) {
-            const __half *ks, *vs;
-            if (u < cached) {
-                const int64_t off = ((int64_t)p * c.rows + fp16_row(u - deep, st.sink, c.Ns, c.R, st.head)) * D;
-                ks = c.k_fp16 + off;
-                vs = c.v_fp16 + off;
-            } else {
-                const int64_t off = (int64_t)(first + u - cached) * x.kv_stride + h * D;
-                ks = x.k + off;
-                vs = x.v + off;
-            }
-            kv = *reinterpret_cast<const uint4 *>(ks + 8 * c8);
-            vv = *reinterpret_cast<const uint4 *>(vs + 8 * c8);
-        }
-        *reinterpret_cast<uint4 *>(tile + image_at(t, c8)) = kv;
-        *reinterpret_cast<uint4 *>(sv + t * VS + 8 * c8) = vv;
-    }
-    __syncthreads();
-    for (int i = tid; i < D * 16; i += kStageThreads) {
-        const int ch = i & (D - 1), t8 = i >> 7;              // 8 tokens of one channel
-        uint32_t w[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const __half2 v = __halves2half2(sv[(8 * t8 + 2 * k) * VS + ch], sv[(8 * t8 + 2 * k + 1) * VS + ch]);
-            w[k] = *reinterpret_cast<const uint32_t *>(&v);
-        }
-        *reinterpret_cast<uint4 *>(tile + kImage + image_at(ch, t8)) = make_uint4(w[0], w[1], w[2], w[3]);
-    }
-}
 
 // -------------------------------------------------- barriers, tensor memory ---
 
@@ -158,35 +86,48 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t phase, volatile 
     return true;
 }
 
+// Waits for a copy that nobody needs any more, about 2 s at most.
+__device__ __forceinline__ void bar_drain(uint32_t bar, uint32_t phase)
+{
+    const long long start = clock64();
+    while (!bar_try(bar, phase) && clock64() - start < kWaitCycles) {}
+}
+
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar)
 {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
                  ::"r"(dst), "l"(src), "r"(bytes), "r"(bar) : "memory");
 }
 
-// Shared-memory operand: K-major rows of 128 bytes, 128-byte swizzle, groups of
-// eight rows 1024 bytes apart.
-__device__ __forceinline__ uint64_t operand(uint32_t addr)
+__device__ __forceinline__ uint64_t operand(uint32_t addr, uint64_t leading, uint64_t stride, uint64_t swizzle)
 {
-    return (uint64_t)((addr & 0x3ffffu) >> 4) | (uint64_t)1 << 16 | (uint64_t)(1024 >> 4) << 32 |
-           (uint64_t)1 << 46 | (uint64_t)2 << 61;
+    return (uint64_t)((addr & 0x3ffffu) >> 4) | (leading >> 4) << 16 | (stride >> 4) << 32 | (uint64_t)1 << 46 | swizzle << 61;
 }
 
-// fp16 x fp16 -> fp32, both K-major, M = 128, N = 128.
-constexpr uint32_t kIdesc = (1u << 4) | ((128u / 8) << 17) | ((128u / 16) << 24);
+// Queries and keys: K-major, 128-byte rows and swizzle, eight rows 1024 bytes apart.
+__device__ __forceinline__ uint64_t by_channel(uint32_t addr) { return operand(addr, 16, 1024, 2); }
+// Their low tiles: K-major, 32-byte rows and swizzle, eight rows 256 bytes apart.
+__device__ __forceinline__ uint64_t by_channel_low(uint32_t addr) { return operand(addr, 16, 256, 6); }
+// Values, [token][channel] with the tokens as K: MN-major, panels of 64 channels
+// kImage / 2 apart, eight tokens 1024 bytes apart.
+__device__ __forceinline__ uint64_t by_token(uint32_t addr) { return operand(addr, kImage / 2, 1024, 2); }
+
+// fp16 x fp16 -> fp32, M = 128, N = 128; both K-major, or B MN-major.
+constexpr uint32_t kIdescK = (1u << 4) | ((128u / 8) << 17) | ((128u / 16) << 24);
+constexpr uint32_t kIdescMN = kIdescK | 1u << 16;
 
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t accumulate)
 {
     asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
                  "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-                 ::"r"(d), "l"(a), "l"(b), "r"(kIdesc), "r"(accumulate) : "memory");
+                 ::"r"(d), "l"(a), "l"(b), "r"(kIdescK), "r"(accumulate) : "memory");
 }
 
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t accumulate)
 {
     asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
                  "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-                 ::"r"(d), "r"(a), "l"(b), "r"(kIdesc), "r"(accumulate) : "memory");
+                 ::"r"(d), "r"(a), "l"(b), "r"(kIdescMN), "r"(accumulate) : "memory");
 }
 
 // The barrier completes a phase when every matrix instruction issued so far has.
@@ -207,15 +148,21 @@ __device__ __forceinline__ void tm_load32(uint32_t addr, uint32_t (&r)[32])
                  : "r"(addr));
 }
 
-__device__ __forceinline__ void tm_store32(uint32_t addr, const uint32_t (&r)[32])
+__device__ __forceinline__ void tm_load16(uint32_t addr, uint32_t (&r)[16])
 {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-                 "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
-                 "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};"
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                 : "r"(addr));
+}
+
+__device__ __forceinline__ void tm_store16(uint32_t addr, const uint32_t (&r)[16])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+                 "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};"
                  ::"r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-                 "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
-                 "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
-                 "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]) : "memory");
+                 "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]) : "memory");
 }
 
 __device__ __forceinline__ void tm_wait_load() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
@@ -223,62 +170,244 @@ __device__ __forceinline__ void tm_wait_store() { asm volatile("tcgen05.wait::st
 __device__ __forceinline__ void tm_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tm_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
-// -------------------------------------------------------------- attention ---
+// ----------------------------------------------------------------- common ---
 
-struct TcOut {
-    const uint8_t *tiles;
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// Largest of 64 scores.
+__device__ __forceinline__ float half_max(const uint32_t (&s)[2][32])
+{
+    float mx[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const uint32_t *e = &s[q >> 1][16 * (q & 1)];
+        mx[q] = fmaxf(__uint_as_float(e[0]), __uint_as_float(e[1]));
+#pragma unroll
+        for (int k = 2; k < 16; k += 2)
+            mx[q] = max3(mx[q], __uint_as_float(e[k]), __uint_as_float(e[k + 1]));
+    }
+    return fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
+}
+
+// {lo half: x0, hi half: x1}, to nearest, for values that are in range.
+__device__ __forceinline__ uint32_t pack(float x0, float x1)
+{
+    uint32_t d;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(x1), "f"(x0));
+    return d;
+}
+
+// Whether any of the 256 threads of team i (barrier 1 + i) says so.
+__device__ __forceinline__ bool team_any(int i, bool said)
+{
+    uint32_t any;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %2, 0;\n\t"
+                 "barrier.cta.red.or.pred.aligned q, %1, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(any) : "r"(1 + i), "r"((uint32_t)said) : "memory");
+    return any != 0;
+}
+
+struct TcArgs {
+    const uint8_t *tiles, *channels;
     int tiles_per_pair, pair0, S;
-    int rows;                 // query rows a pair has room for in the partial results
+    int row0, rows;           // first query row of this launch, and rows a pair has room for in the results
     __half *out;
-    float *o;                 // [pairs of this launch][rows][S][D] (S > 1)
-    float2 *ml;               // [pairs of this launch][rows][S]
+    float *o;                 // [pairs of this launch][rows][S][D] (attention, S > 1)
+    float2 *ml;               // [pairs of this launch][rows][S] (weights: [2 S])
+    float *ls;                // weights: [pairs of this launch][rows][units]
+    int unit, units;
 };
+
+// The 16 key channels of each pair whose keys also get a low part: those with
+// the largest scales in up to 32 of its pages (no result depends on which they
+// are but for its last bits).
+__global__ void __launch_bounds__(kHeadDim) channels_kernel(PagedArgs c, ChunkArgs x, int pair0, uint8_t *channels)
+{
+    __shared__ float top[kHeadDim];
+    const int p = pair0 + blockIdx.x, ch = threadIdx.x;
+    int first, T;
+    PagedState st;
+    if (!sequence(c, x, p / c.Hkv, first, T, st))
+        return;
+    const int n = min(st.held, 32);
+    float most = 0.0f;
+    for (int i = 0; i < n; ++i) {
+        const unsigned char *rec = page_record(c, p, (int)((int64_t)st.held * i / n));
+        if (rec)
+            most = fmaxf(most, c.meta ? meta_load<1>(rec, ch) : meta_load<0>(rec, ch));
+    }
+    top[ch] = most;
+    __syncthreads();
+    int rank = 0;
+    for (int i = 0; i < kHeadDim; ++i)
+        rank += top[i] > most || (top[i] == most && i < ch);
+    if (rank < kChannels)
+        channels[blockIdx.x * kChannels + rank] = (uint8_t)ch;
+}
+
+// Eight halves of a run of 16 (elements of places 8 half .. 8 half + 7).
+template <int BITS>
+__device__ __forceinline__ uint4 pick_places(const uint4 (&run)[2], int half)
+{
+    const __half *e = reinterpret_cast<const __half *>(run);
+    uint32_t a[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const __half2 v = __halves2half2(e[run_element(BITS, 2 * i)], e[run_element(BITS, 2 * i + 1)]);
+        a[i] = *reinterpret_cast<const uint32_t *>(&v);
+    }
+    return half ? make_uint4(a[4], a[5], a[6], a[7]) : make_uint4(a[0], a[1], a[2], a[3]);
+}
+
+// The block's query rows (row0 on, `count` of them exist) as operand images of
+// mtiles M tiles, channels in the tiles' order; low: the picked channels alone.
+template <int THREADS>
+__device__ __forceinline__ void load_queries(const PagedArgs &c, const ChunkArgs &x, int h, int first, int row0, int rows,
+                                             int mtiles, uint8_t (*q)[kImage], uint8_t (*q_low)[kLow], const uint8_t *channels)
+{
+    constexpr int D = kHeadDim;
+    auto row_of = [&](int row) {
+        const int t = row / c.g;
+        return x.q + (int64_t)(first + t) * x.q_stride + (h * c.g + row - t * c.g) * D;
+    };
+    for (int i = threadIdx.x; i < mtiles * kMTile * 8; i += THREADS) {
+        const int r = i >> 3, run = i & 7;
+        uint4 v[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+        if (row0 + r < rows) {
+            const uint4 *src = reinterpret_cast<const uint4 *>(row_of(row0 + r) + 16 * run);
+            v[0] = src[0];
+            v[1] = src[1];
+        }
+        uint4 a = v[0], b = v[1];
+        if (c.bits == 2) {
+            a = pick_places<2>(v, 0);
+            b = pick_places<2>(v, 1);
+        } else if (c.bits == 4) {
+            a = pick_places<4>(v, 0);
+            b = pick_places<4>(v, 1);
+        }
+        *reinterpret_cast<uint4 *>(q[r >> 7] + image_at(r & 127, 2 * run)) = a;
+        *reinterpret_cast<uint4 *>(q[r >> 7] + image_at(r & 127, 2 * run + 1)) = b;
+    }
+    if (!q_low)
+        return;
+    for (int i = threadIdx.x; i < mtiles * kMTile * 2; i += THREADS) {
+        const int r = i >> 1, half = i & 1;
+        uint32_t w[4] = {0u, 0u, 0u, 0u};
+        if (row0 + r < rows) {
+            const __half *src = row_of(row0 + r);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const __half2 v = __halves2half2(src[channels[8 * half + 2 * e]], src[channels[8 * half + 2 * e + 1]]);
+                w[e] = *reinterpret_cast<const uint32_t *>(&v);
+            }
+        }
+        *reinterpret_cast<uint4 *>(q_low[r >> 7] + low_at(r & 127, half)) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
+// One lane of the warp issues.  The whole warp runs the loops around it, so that
+// the operands stay uniform: worked out by one diverged thread, they cost more
+// than the products they start.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
+    return ok != 0;
+}
+
+// S[128 x 128] = Q K^T in tensor memory at d, eight steps of 16 channels.
+__device__ __forceinline__ void mma_scores(uint32_t d, uint64_t q, uint64_t k, uint32_t accumulate)
+{
+#pragma unroll
+    for (int ks = 0; ks < 8; ++ks) {
+        const uint32_t off = ((ks >> 2) * (kImage / 2) + (ks & 3) * 32) >> 4;
+        mma_ss(d, q + off, k + off, accumulate | (ks > 0));
+    }
+}
+
+// What a block works on.
+struct Job {
+    int p, h, first, T;
+    int rows, row0;           // query rows of the pair, first of the block
+    int deep, rowed;          // page tokens, other cached tokens
+    int np;                   // page tiles of the pair
+    int t0, n;                // tiles of this block: first, and how many
+};
+
+// False when the block has nothing to do (or must not do it).
+__device__ __forceinline__ bool job_of(const PagedArgs &c, const ChunkArgs &x, const TcArgs &d, Job &j)
+{
+    j.p = d.pair0 + blockIdx.y;
+    const int b = j.p / c.Hkv;
+    j.h = j.p % c.Hkv;
+    PagedState st;
+    if (!sequence(c, x, b, j.first, j.T, st)) {
+        if (threadIdx.x == 0 && blockIdx.x == 0 && blockIdx.z == 0)
+            atomicOr(c.control, KIVI_STATUS_BAD_STATE);
+        return false;
+    }
+    j.rows = j.T * c.g;
+    j.row0 = d.row0 + blockIdx.x * kRows;
+    if (j.row0 >= j.rows)
+        return false;
+    j.deep = st.held * c.G;
+    j.rowed = st.sink + st.window;
+    const int seen = !x.k ? 0 : x.full ? j.T : min(j.T, (j.row0 + kRows - 1) / c.g + 1);
+    j.np = (j.deep + kTok - 1) / kTok;
+    const int tiles = j.np + (j.rowed + seen + kTok - 1) / kTok;
+    j.t0 = (int)((int64_t)tiles * blockIdx.z / d.S);
+    j.n = (int)((int64_t)tiles * (blockIdx.z + 1) / d.S) - j.t0;
+    return true;
+}
+
+// Columns of tile t (of the pair) that query row `row` sees.
+__device__ __forceinline__ int columns_of(const PagedArgs &c, const ChunkArgs &x, const Job &j, int t, int tok)
+{
+    if (t < j.np)
+        return j.deep - t * kTok;
+    const int fresh = !x.k ? 0 : x.full ? j.T : min(j.T, tok + 1);
+    return j.rowed + fresh - (t - j.np) * kTok;
+}
+
+// -------------------------------------------------------------- attention ---
 
 struct TcSmem {
     uint8_t q[2][kImage];
     uint8_t k[kStages][kImage];
     uint8_t v[kStages][kImage];
+    uint8_t q_low[2][kLow];
+    uint8_t k_low[kStages][kLow];
     uint64_t k_full[kStages], k_free[kStages], v_full[kStages], v_free[kStages];
+    float rows[2][2][kMTile];     // per team and half: a row's maximum, at the end its sum
     uint64_t s_full[2], p_full[2];
     uint32_t tmem;
     int failed;
 };
+// the join of the two teams of one M tile: [128][D + 4] floats from q[1] on, and (m, l) and a factor per row in q_low[1]
+static_assert(kMTile * (kHeadDim + 4) * 4 <= 3 * kImage, "join buffer");
 
 template <bool CAP>
-__global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(PagedArgs c, ChunkArgs x, TcOut d)
+__global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(PagedArgs c, ChunkArgs x, TcArgs d)
 {
     constexpr int D = kHeadDim;
     extern __shared__ uint8_t smem_raw[];
     TcSmem &sm = *reinterpret_cast<TcSmem *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int p = d.pair0 + blockIdx.y, b = p / c.Hkv, h = p % c.Hkv;
-    int first, T;
-    PagedState st;
-    if (!sequence(c, x, b, first, T, st)) {
-        if (tid == 0 && blockIdx.x == 0 && blockIdx.z == 0)
-            atomicOr(c.control, KIVI_STATUS_BAD_STATE);
+    Job job;
+    if (!job_of(c, x, d, job))
         return;
-    }
-    const int rows = T * c.g, row0 = blockIdx.x * kRows;
-    if (row0 >= rows)
-        return;
-    const int cached = st.held * c.G + st.sink + st.window;
-    const int seen = !x.k ? 0 : x.full ? T : min(T, (row0 + kRows - 1) / c.g + 1);
-    const int total = cached + seen;
-    const int tiles = (total + kTok - 1) / kTok;
-    const int t0 = (int)((int64_t)tiles * blockIdx.z / d.S), n = (int)((int64_t)tiles * (blockIdx.z + 1) / d.S) - t0;
-    const int mtiles = rows - row0 > kMTile ? 2 : 1;
+    const int n = job.n;
+    const bool two = job.rows - job.row0 > kMTile;      // two M tiles, or one whose tiles the warpgroups share
+    const bool low = c.fmt == 0;
 
-    // queries, swizzled like the keys; rows behind the last one count as zero
-    for (int i = tid; i < mtiles * kMTile * 16; i += kTcThreads) {
-        const int r = i >> 4, c8 = i & 15, row = row0 + r;
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (row < rows) {
-            const int t = row / c.g, hh = row - t * c.g;
-            v = *reinterpret_cast<const uint4 *>(x.q + (int64_t)(first + t) * x.q_stride + (h * c.g + hh) * D + 8 * c8);
-        }
-        *reinterpret_cast<uint4 *>(sm.q[r >> 7] + image_at(r & 127, c8)) = v;
-    }
+    load_queries<kTcThreads>(c, x, job.h, job.first, job.row0, job.rows, two ? 2 : 1, sm.q, low ? sm.q_low : nullptr,
+                 d.channels + blockIdx.y * kChannels);
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) {
             bar_init(smem_addr(&sm.k_full[i]), 1);
@@ -288,7 +417,383 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(PagedArgs c, ChunkArg
         }
         for (int i = 0; i < 2; ++i) {
             bar_init(smem_addr(&sm.s_full[i]), 1);
-            bar_init(smem_addr(&sm.p_full[i]), kMTile);
+            bar_init(smem_addr(&sm.p_full[i]), 2 * kMTile);
+        }
+        sm.failed = 0;
+    }
+    if (warp == 16) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&sm.tmem)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    tm_fence_before();
+    __syncthreads();
+    tm_fence_after();
+    const uint32_t tm = sm.tmem;                  // columns: S/P of warpgroup 0, of 1, O of 0, of 1
+    volatile int *failed = &sm.failed;
+    auto paged = [&](int j) { return job.t0 + j < job.np; };
+
+    if (warp == 17) {
+        if (lane == 0) {                          // fetches the tiles
+            const uint8_t *src = d.tiles + ((int64_t)blockIdx.y * d.tiles_per_pair + job.t0) * kTileBytes;
+            int keys = 0, values = 0;             // tiles asked for
+            for (int j = 0; j < n; ++j, src += kTileBytes) {
+                const int s = j % kStages;
+                const uint32_t free_phase = ((j / kStages) & 1) ^ 1;      // the first round passes at once
+                if (!bar_wait(smem_addr(&sm.k_free[s]), free_phase, failed))
+                    break;
+                const bool with_low = low && paged(j);
+                bar_expect(smem_addr(&sm.k_full[s]), kImage + (with_low ? kLow : 0));
+                bulk_load(smem_addr(sm.k[s]), src, kImage, smem_addr(&sm.k_full[s]));
+                if (with_low)
+                    bulk_load(smem_addr(sm.k_low[s]), src + 2 * kImage, kLow, smem_addr(&sm.k_full[s]));
+                keys = j + 1;
+                if (!bar_wait(smem_addr(&sm.v_free[s]), free_phase, failed))
+                    break;
+                bar_expect(smem_addr(&sm.v_full[s]), kImage);
+                bulk_load(smem_addr(sm.v[s]), src + kImage, kImage, smem_addr(&sm.v_full[s]));
+                values = j + 1;
+            }
+            if (*failed) {                        // leave no copy in flight: wait, with a limit, for the last ones
+                for (int j = max(0, keys - kStages); j < keys; ++j)
+                    bar_drain(smem_addr(&sm.k_full[j % kStages]), (j / kStages) & 1);
+                for (int j = max(0, values - kStages); j < values; ++j)
+                    bar_drain(smem_addr(&sm.v_full[j % kStages]), (j / kStages) & 1);
+            }
+        }
+    } else if (warp == 16) {
+        if (n > 0) {                              // issues the matrix instructions
+            const bool leader = elect_one();
+            const uint64_t q_at = by_channel(smem_addr(sm.q[0])), k_at = by_channel(smem_addr(sm.k[0]));
+            const uint64_t q_low_at = by_channel_low(smem_addr(sm.q_low[0])), k_low_at = by_channel_low(smem_addr(sm.k_low[0]));
+            const uint64_t v_at = by_token(smem_addr(sm.v[0]));
+            // scores of tile j into S of team i, against M tile m; then (team i of) bar
+            auto scores = [&](int i, int m, int j) {
+                const int s = j % kStages;
+                const bool with_low = low && paged(j);
+                if (leader) {
+                    if (with_low)
+                        mma_ss(tm + 128 * i, q_low_at + m * (kLow >> 4), k_low_at + s * (kLow >> 4), 0);
+                    mma_scores(tm + 128 * i, q_at + m * (kImage >> 4), k_at + s * (kImage >> 4), with_low);
+                }
+            };
+            auto values = [&](int i, int j, bool first) {
+                const uint64_t v = v_at + (j % kStages) * (kImage >> 4);
+                if (leader) {
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks)
+                        mma_ts(tm + 256 + 128 * i, tm + 128 * i + 8 * ks, v + (ks * 16 * 128 >> 4), !first || ks > 0);
+                }
+            };
+            auto commit = [&](uint64_t *bar) {
+                if (leader)
+                    mma_commit(smem_addr(bar));
+            };
+            auto there = [&](uint64_t *bar, int phase) {
+                return (bool)__all_sync(0xffffffffu, bar_wait(smem_addr(bar), phase & 1, failed));
+            };
+            auto keys_there = [&](int j) { return there(&sm.k_full[j % kStages], j / kStages); };
+            auto values_there = [&](int j) { return there(&sm.v_full[j % kStages], j / kStages); };
+            bool ok = keys_there(0);
+            if (two) {
+                if (ok) {
+                    for (int i = 0; i < 2; ++i) {
+                        scores(i, i, 0);
+                        commit(&sm.s_full[i]);
+                    }
+                    commit(&sm.k_free[0]);
+                }
+                for (int j = 0; ok && j < n; ++j) {
+                    const bool more = j + 1 < n;
+                    ok = values_there(j) && (!more || keys_there(j + 1));
+                    for (int i = 0; ok && i < 2; ++i) {
+                        ok = there(&sm.p_full[i], j);
+                        if (!ok)
+                            break;
+                        tm_fence_after();
+                        values(i, j, j == 0);
+                        if (more)
+                            scores(i, i, j + 1);
+                        commit(&sm.s_full[i]);
+                    }
+                    if (ok) {
+                        commit(&sm.v_free[j % kStages]);
+                        if (more)
+                            commit(&sm.k_free[(j + 1) % kStages]);
+                    }
+                }
+            } else {
+                // tile j belongs to team j & 1
+                for (int j = 0; ok && j < min(n, 2); ++j) {
+                    ok = j == 0 || keys_there(j);
+                    if (ok) {
+                        scores(j, 0, j);
+                        commit(&sm.s_full[j]);
+                        commit(&sm.k_free[j]);
+                    }
+                }
+                for (int j = 0; ok && j < n; ++j) {
+                    const int i = j & 1;
+                    const bool more = j + 2 < n;
+                    ok = values_there(j) && (!more || keys_there(j + 2)) && there(&sm.p_full[i], j >> 1);
+                    if (!ok)
+                        break;
+                    tm_fence_after();
+                    values(i, j, j < 2);
+                    if (more)
+                        scores(i, 0, j + 2);
+                    commit(&sm.s_full[i]);
+                    commit(&sm.v_free[j % kStages]);
+                    if (more)
+                        commit(&sm.k_free[(j + 2) % kStages]);
+                }
+            }
+        }
+    } else if (warp < 16) {
+        // softmax: a thread has columns 64 half .. + 63 of one query row (its TMEM lane)
+        const int i = warp >> 3, half = (warp >> 2) & 1;
+        const uint32_t lanes = (uint32_t)(warp & 3) << 21;             // 32 lanes a warp, lane field from bit 16
+        const uint32_t ts = tm + 128 * i + lanes, to = tm + 256 + 128 * i + 64 * half + lanes;
+        const int r = (warp & 3) * 32 + lane, row = job.row0 + (two ? i * kMTile : 0) + r;
+        const int tok = row / c.g, hh = row - tok * c.g;
+        const int mine = two ? n : (n - i + 1) / 2;                    // tiles of this team
+        const float page_times = low ? 2.0f : c.fp8_k_scale, page_value = low ? 2.0f : c.fp8_v_scale;
+        float *shared = sm.rows[i][half], *theirs = sm.rows[i][half ^ 1];
+        float m = -INFINITY, l = 0.0f;                                  // l: of this half
+        bool in_pages = false, lost = false;                           // O is in units of page_value; a wait gave up
+        for (int e = 0; e < mine; ++e) {
+            const int j = two ? e : 2 * e + i, t = job.t0 + j;
+            const bool ok = __all_sync(0xffffffffu, bar_wait(smem_addr(&sm.s_full[i]), e & 1, failed));
+            tm_fence_after();
+            uint32_t s[2][32];
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+                tm_load32(ts + 64 * half + 32 * q, s[q]);
+            tm_wait_load();
+            const float times = paged(j) ? page_times : 1.0f;
+            if constexpr (CAP) {
+#pragma unroll
+                for (int q = 0; q < 2; ++q)
+#pragma unroll
+                    for (int k = 0; k < 32; ++k)
+                        s[q][k] = __float_as_uint(score_log2(__uint_as_float(s[q][k]) * times, x));
+            }
+            const float scale = CAP ? 1.0f : x.scale_log2 * times;
+            const int left = columns_of(c, x, job, t, tok) - 64 * half;
+            if (left < 64) {
+#pragma unroll
+                for (int q = 0; q < 2; ++q)
+#pragma unroll
+                    for (int k = 0; k < 32; ++k)
+                        if (32 * q + k >= left)
+                            s[q][k] = 0xff800000u;                      // -inf
+            }
+            const float top = half_max(s) * scale;
+            const bool leaves = in_pages && !paged(j);                   // O becomes plain
+            in_pages = paged(j);
+            // One barrier per tile: both halves have read S (P goes over it), and
+            // a maximum that ran ahead (also the first one, m = -inf) is known to
+            // the whole team.
+            tm_fence_before();
+            const bool move = team_any(i, !ok || top - m > kRescale);
+            tm_fence_after();
+            if (move || leaves) {
+                shared[r] = top;
+                asm volatile("barrier.cta.sync.aligned %0, 256;" ::"r"(1 + i) : "memory");
+                const float both = fmaxf(top, theirs[r]);
+                if (team_any(i, !ok)) {
+                    lost = true;
+                    break;
+                }
+                const bool grown = both - m > kRescale;
+                const float m1 = grown ? both : m;
+                const float alpha = grown && m > -INFINITY ? ex2(m - m1) : 1.0f;
+                m = m1;
+                l *= alpha;
+                const float factor = leaves ? alpha * page_value : alpha;
+                if (e > 0) {
+                    // O is at rest: the phase just waited for ends after the last P V
+#pragma unroll 1
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t o[16];
+                        tm_load16(to + 16 * q, o);
+                        tm_wait_load();
+#pragma unroll
+                        for (int k = 0; k < 16; ++k)
+                            o[k] = __float_as_uint(__uint_as_float(o[k]) * factor);
+                        tm_store16(to + 16 * q, o);
+                    }
+                }
+            }
+            const float ms = m == -INFINITY ? 0.0f : m;
+            const float2 scale2 = make_float2(scale, scale), ms2 = make_float2(-ms, -ms);
+            float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                uint32_t pk[16];
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                    float2 a = __ffma2_rn(make_float2(__uint_as_float(s[q][2 * k]), __uint_as_float(s[q][2 * k + 1])), scale2, ms2);
+                    a = make_float2(ex2(a.x), ex2(a.y));
+                    sum[k & 1] = __fadd2_rn(sum[k & 1], a);
+                    pk[k] = pack(a.x, a.y);
+                }
+                tm_store16(ts + 32 * half + 16 * q, pk);
+            }
+            l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+            tm_wait_store();
+            tm_fence_before();
+            bar_arrive(smem_addr(&sm.p_full[i]));
+        }
+        if (mine > 0 && !lost)
+            __all_sync(0xffffffffu, bar_wait(smem_addr(&sm.s_full[i]), mine & 1, failed));       // the last P V
+        tm_fence_after();
+        // the halves' sums, and with one M tile the teams' parts
+        float w = in_pages ? page_value : 1.0f, w1 = 0.0f;              // factors of this O and of the other team's
+        shared[r] = l;
+        asm volatile("barrier.cta.sync.aligned %0, 256;" ::"r"(1 + i) : "memory");
+        l += theirs[r];
+        float *xo = reinterpret_cast<float *>(sm.q[1]) + r * (D + 4) + 64 * half;
+        float2 *xml = reinterpret_cast<float2 *>(sm.q_low[1]) + r;
+        if (!two) {
+            // Team 1 hands over its part, if it had a tile.  Its last commit came
+            // after the last scores were issued, so the key buffers are free by
+            // then.
+            if (i == 1) {
+#pragma unroll 1
+                for (int q = 0; q < (mine > 0 ? 4 : 0); ++q) {
+                    uint32_t o[16];
+                    __syncwarp();
+                    tm_load16(to + 16 * q, o);
+                    tm_wait_load();
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        *reinterpret_cast<uint4 *>(xo + 16 * q + 4 * k) = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                }
+                if (half == 0) {
+                    xml[0] = make_float2(m, l);
+                    xml[kMTile].x = w;
+                }
+            }
+            asm volatile("barrier.cta.sync.aligned 3, 512;" ::: "memory");
+            if (i == 0) {
+                const float2 other = xml[0];
+                const float M = fmaxf(m, other.x), at = M == -INFINITY ? 0.0f : M;
+                const float f0 = ex2(m - at), f1 = ex2(other.x - at);
+                w1 = xml[kMTile].x * f1;
+                w *= f0;
+                l = l * f0 + other.y * f1;
+                m = M;
+            }
+        }
+        const bool writes = (two || i == 0) && row < job.rows;
+        const float inv = d.S == 1 ? (l > 0.0f ? 1.0f / l : 0.0f) : 1.0f;
+        const int64_t part = ((int64_t)blockIdx.y * d.rows + (row - d.row0)) * d.S + blockIdx.z;
+        const int64_t at = (int64_t)(job.first + tok) * (c.Hkv * c.g) + job.h * c.g + hh;
+        // a run's places hold the channels of its stored positions, in the run's order
+#pragma unroll 1
+        for (int q = 0; q < 4; ++q) {
+            uint32_t o[16];
+            __syncwarp();
+            if (mine > 0 && (two || i == 0)) {
+                tm_load16(to + 16 * q, o);
+                tm_wait_load();
+            } else {
+#pragma unroll
+                for (int k = 0; k < 16; ++k)
+                    o[k] = 0u;
+            }
+            if (!writes)
+                continue;
+            float f[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+                f[k] = __uint_as_float(o[k]) * w;
+            if (w1 != 0.0f) {
+#pragma unroll
+                for (int k = 0; k < 16; ++k)
+                    f[k] = fmaf(xo[16 * q + k], w1, f[k]);
+            }
+            auto put = [&](auto bits) {
+                constexpr int BITS = decltype(bits)::value;
+                // pairs of neighbouring stored positions are neighbouring channels
+#pragma unroll
+                for (int k = 0; k < 16; k += 2) {
+                    int p0 = 0, p1 = 0;                 // their places in the run
+#pragma unroll
+                    for (int z = 0; z < 16; ++z) {
+                        if (run_element(BITS, z) == k)
+                            p0 = z;
+                        if (run_element(BITS, z) == k + 1)
+                            p1 = z;
+                    }
+                    const float a0 = f[p0] * inv, a1 = f[p1] * inv;
+                    const int ch = value_channel(BITS, c.G, BITS == 8, 64 * half + 16 * q + k);
+                    if (d.S == 1)
+                        *reinterpret_cast<uint32_t *>(d.out + at * D + ch) = pack_sat(a0, a1);
+                    else
+                        *reinterpret_cast<float2 *>(d.o + part * D + ch) = make_float2(a0, a1);
+                }
+            };
+            if (c.bits == 2)
+                put(std::integral_constant<int, 2>{});
+            else if (c.bits == 4)
+                put(std::integral_constant<int, 4>{});
+            else
+                put(std::integral_constant<int, 8>{});
+        }
+        if (d.S > 1 && writes && half == 0)
+            d.ml[part] = make_float2(m, l);
+    }
+    tm_fence_before();
+    __syncthreads();
+    if (tid == 0 && sm.failed)
+        atomicOr(c.control, KIVI_STATUS_WAIT_TIMEOUT);
+    if (warp == 16) {
+        __syncwarp();
+        tm_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tm));
+    }
+}
+
+// ---------------------------------------------------------------- weights ---
+
+struct WeighSmem {
+    uint8_t q[2][kImage];
+    uint8_t k[kStages][kImage];
+    uint8_t k_low[kStages][kImage];
+    uint64_t k_full[kStages], k_free[kStages];
+    uint64_t s_full[4], s_free[4];
+    uint32_t tmem;
+    int failed;
+};
+
+// Step e is the scores of one M tile against one token tile (two M tiles: M tile
+// e & 1, tile e / 2; one: tile e), in S buffer e & 3, read by warpgroup e & 1.
+template <bool CAP, int UNIT>
+__global__ void __launch_bounds__(kWeighThreads, 1) tc_weigh_kernel(PagedArgs c, ChunkArgs x, TcArgs d)
+{
+    extern __shared__ uint8_t smem_raw[];
+    WeighSmem &sm = *reinterpret_cast<WeighSmem *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    Job job;
+    if (!job_of(c, x, d, job))
+        return;
+    const int n = job.n;
+    const bool two = job.rows - job.row0 > kMTile;
+    const bool low = c.fmt == 0;
+    const int steps = two ? 2 * n : n;
+
+    load_queries<kWeighThreads>(c, x, job.h, job.first, job.row0, job.rows, two ? 2 : 1, sm.q, nullptr, nullptr);
+    if (tid == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            bar_init(smem_addr(&sm.k_full[i]), 1);
+            bar_init(smem_addr(&sm.k_free[i]), 1);
+        }
+        for (int i = 0; i < 4; ++i) {
+            bar_init(smem_addr(&sm.s_full[i]), 1);
+            bar_init(smem_addr(&sm.s_free[i]), kMTile);
         }
         sm.failed = 0;
     }
@@ -301,204 +806,132 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(PagedArgs c, ChunkArg
     tm_fence_before();
     __syncthreads();
     tm_fence_after();
-    const uint32_t tm = sm.tmem;                  // columns: S/P of tile 0, of tile 1, O of tile 0, of tile 1
+    const uint32_t tm = sm.tmem;
     volatile int *failed = &sm.failed;
+    auto paged = [&](int j) { return job.t0 + j < job.np; };
 
     if (warp == 9) {
-        if (lane == 0) {                          // fetches the tiles
-            const uint8_t *src = d.tiles + ((int64_t)blockIdx.y * d.tiles_per_pair + t0) * kTileBytes;
-            int sent = 0;
+        if (lane == 0) {
+            const uint8_t *src = d.tiles + ((int64_t)blockIdx.y * d.tiles_per_pair + job.t0) * kTileBytes;
+            int keys = 0;
             for (int j = 0; j < n; ++j, src += kTileBytes) {
                 const int s = j % kStages;
-                const uint32_t free_phase = ((j / kStages) & 1) ^ 1;      // the first round passes at once
-                if (!bar_wait(smem_addr(&sm.k_free[s]), free_phase, failed))
+                if (!bar_wait(smem_addr(&sm.k_free[s]), ((j / kStages) & 1) ^ 1, failed))
                     break;
-                bar_expect(smem_addr(&sm.k_full[s]), kImage);
+                const bool with_low = low && paged(j);
+                bar_expect(smem_addr(&sm.k_full[s]), with_low ? 2 * kImage : kImage);
                 bulk_load(smem_addr(sm.k[s]), src, kImage, smem_addr(&sm.k_full[s]));
-                if (!bar_wait(smem_addr(&sm.v_free[s]), free_phase, failed)) {
-                    sent = -j - 1;                // the keys of tile j are on their way, its values are not
-                    break;
-                }
-                bar_expect(smem_addr(&sm.v_full[s]), kImage);
-                bulk_load(smem_addr(sm.v[s]), src + kImage, kImage, smem_addr(&sm.v_full[s]));
-                sent = j + 1;
+                if (with_low)
+                    bulk_load(smem_addr(sm.k_low[s]), src + kImage, kImage, smem_addr(&sm.k_full[s]));
+                keys = j + 1;
             }
-            if (*failed) {                        // leave no copy in flight: wait, with a limit, for the last ones
-                const int upto = sent < 0 ? -sent : sent;
-                for (int j = max(0, upto - kStages); j < upto; ++j) {
-                    const long long start = clock64();
-                    const uint32_t phase = (j / kStages) & 1;
-                    while (!bar_try(smem_addr(&sm.k_full[j % kStages]), phase) && clock64() - start < kWaitCycles) {}
-                    if (!(sent < 0 && j == upto - 1))
-                        while (!bar_try(smem_addr(&sm.v_full[j % kStages]), phase) && clock64() - start < kWaitCycles) {}
-                }
-            }
+            if (*failed)
+                for (int j = max(0, keys - kStages); j < keys; ++j)
+                    bar_drain(smem_addr(&sm.k_full[j % kStages]), (j / kStages) & 1);
         }
     } else if (warp == 8) {
-        if (lane == 0 && n > 0) {                 // issues the matrix instructions
-            auto qk = [&](int i, int s) {
-#pragma unroll
-                for (int ks = 0; ks < 8; ++ks) {
-                    const uint32_t off = (ks >> 2) * (kImage / 2) + (ks & 3) * 32;
-                    mma_ss(tm + 128 * i, operand(smem_addr(sm.q[i]) + off), operand(smem_addr(sm.k[s]) + off), ks > 0);
-                }
-            };
-            bool ok = bar_wait(smem_addr(&sm.k_full[0]), 0, failed);
-            if (ok) {
-                for (int i = 0; i < mtiles; ++i) {
-                    qk(i, 0);
-                    mma_commit(smem_addr(&sm.s_full[i]));
-                }
-                mma_commit(smem_addr(&sm.k_free[0]));
-            }
-            for (int j = 0; ok && j < n; ++j) {
-                const int s = j % kStages, s1 = (j + 1) % kStages;
-                const bool more = j + 1 < n;
-                ok = bar_wait(smem_addr(&sm.v_full[s]), (j / kStages) & 1, failed) &&
-                     (!more || bar_wait(smem_addr(&sm.k_full[s1]), ((j + 1) / kStages) & 1, failed));
-                for (int i = 0; ok && i < mtiles; ++i) {
-                    ok = bar_wait(smem_addr(&sm.p_full[i]), j & 1, failed);
-                    if (!ok)
-                        break;
-                    tm_fence_after();
-#pragma unroll
-                    for (int ks = 0; ks < 8; ++ks) {
-                        const uint32_t off = (ks >> 2) * (kImage / 2) + (ks & 3) * 32;
-                        mma_ts(tm + 256 + 128 * i, tm + 128 * i + 8 * ks, operand(smem_addr(sm.v[s]) + off), j > 0 || ks > 0);
-                    }
-                    if (more)
-                        qk(i, s1);
-                    mma_commit(smem_addr(&sm.s_full[i]));
-                }
-                if (ok) {
-                    mma_commit(smem_addr(&sm.v_free[s]));
-                    if (more)
-                        mma_commit(smem_addr(&sm.k_free[s1]));
-                }
-            }
-        }
-    } else if ((warp >> 2) < mtiles) {
-        // softmax: warpgroup i owns M tile i, a thread one query row (its TMEM lane)
-        const int i = warp >> 2;
-        const uint32_t lanes = (uint32_t)(warp & 3) << 21;             // 32 lanes a warp, lane field from bit 16
-        const uint32_t ts = tm + 128 * i + lanes, to = tm + 256 + 128 * i + lanes;
-        const int row = row0 + i * kMTile + (warp & 3) * 32 + lane;
-        const int tok = row / c.g, hh = row - tok * c.g;
-        // tokens this row sees, from the first of this block's range
-        const int limit = (row < rows && x.k && !x.full ? min(total, cached + tok + 1) : total) - t0 * kTok;
-        const float scale = CAP ? 1.0f : x.scale_log2;
-        float m = -INFINITY, l = 0.0f;
+        const bool leader = elect_one();
+        const uint64_t q_at = by_channel(smem_addr(sm.q[0])), k_at = by_channel(smem_addr(sm.k[0]));
+        const uint64_t k_low_at = by_channel(smem_addr(sm.k_low[0]));
         bool ok = true;
-        for (int j = 0; j < n; ++j) {
-            ok = __all_sync(0xffffffffu, bar_wait(smem_addr(&sm.s_full[i]), j & 1, failed));
+        for (int e = 0; ok && e < steps; ++e) {
+            const int j = two ? e >> 1 : e, m = two ? e & 1 : 0, s = j % kStages;
+            if (!two || m == 0)
+                ok = __all_sync(0xffffffffu, bar_wait(smem_addr(&sm.k_full[s]), (j / kStages) & 1, failed));
+            ok = ok && __all_sync(0xffffffffu, bar_wait(smem_addr(&sm.s_free[e & 3]), ((e >> 2) & 1) ^ 1, failed));
             if (!ok)
                 break;
             tm_fence_after();
-            uint32_t r[4][32];
+            const uint32_t to = tm + 128 * (e & 3);
+            const bool with_low = low && paged(j);
+            if (leader) {
+                if (with_low)
+                    mma_scores(to, q_at + m * (kImage >> 4), k_low_at + s * (kImage >> 4), 0);
+                mma_scores(to, q_at + m * (kImage >> 4), k_at + s * (kImage >> 4), with_low);
+                mma_commit(smem_addr(&sm.s_full[e & 3]));
+                if (!two || m == 1)
+                    mma_commit(smem_addr(&sm.k_free[s]));
+            }
+        }
+    } else {
+        const int i = warp >> 2;
+        const uint32_t lanes = (uint32_t)(warp & 3) << 21;
+        const int row = job.row0 + (two ? i * kMTile : 0) + (warp & 3) * 32 + lane;
+        const int tok = row / c.g;
+        const bool live = row < job.rows;
+        const float page_times = low ? 2.0f : c.fp8_k_scale;
+        float *ls = d.ls + ((int64_t)blockIdx.y * d.rows + (row - d.row0)) * d.units;
+        float m = -INFINITY, l = 0.0f;
+        bool ok = true;
+        for (int e = i; e < steps; e += 2) {
+            const int j = two ? e >> 1 : e, t = job.t0 + j;
+            ok = __all_sync(0xffffffffu, bar_wait(smem_addr(&sm.s_full[e & 3]), (e >> 2) & 1, failed));
+            if (!ok)
+                break;
+            tm_fence_after();
+            const bool page = paged(j);
+            const float times = page ? page_times : 1.0f, scale = CAP ? 1.0f : x.scale_log2 * times;
+            const int left = columns_of(c, x, job, t, tok);
+            float unit_max[kTok / UNIT], unit_sum[kTok / UNIT];
+            uint32_t s[4][32];
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-                tm_load32(ts + 32 * q, r[q]);
+                tm_load32(tm + 128 * (e & 3) + lanes + 32 * q, s[q]);
             tm_wait_load();
-            if constexpr (CAP) {
+            tm_fence_before();
+            bar_arrive(smem_addr(&sm.s_free[e & 3]));
+            float top = -INFINITY;
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
+            for (int q = 0; q < 4; ++q) {
+                if constexpr (CAP) {
 #pragma unroll
                     for (int k = 0; k < 32; ++k)
-                        r[q][k] = __float_as_uint(score_log2(__uint_as_float(r[q][k]), x));
-            }
-            const int left = limit - j * kTok;
-            if (left < kTok) {
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
+                        s[q][k] = __float_as_uint(score_log2(__uint_as_float(s[q][k]) * times, x));
+                }
+                if (left < 32 * q + 32) {
 #pragma unroll
                     for (int k = 0; k < 32; ++k)
                         if (32 * q + k >= left)
-                            r[q][k] = 0xff800000u;                      // -inf
-            }
-            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                            s[q][k] = 0xff800000u;
+                }
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
+                for (int u = 0; u < 32; u += UNIT) {
+                    float mx = -INFINITY, sum0 = 0.0f, sum1 = 0.0f;
 #pragma unroll
-                for (int k = 0; k < 32; ++k)
-                    mx[k & 3] = fmaxf(mx[k & 3], __uint_as_float(r[q][k]));
-            const float tile_max = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-            const bool grown = (tile_max - m) * scale > kRescale;        // also the first time (m = -inf)
-            if (__any_sync(0xffffffffu, grown)) {
-                const float m1 = grown ? tile_max : m;
-                const float alpha = grown && l > 0.0f ? ex2((m - m1) * scale) : 1.0f;
-                m = m1;
-                l *= alpha;
-                if (j > 0) {
-                    // O is at rest: the phase just waited for ends after the last P V
-#pragma unroll 1
-                    for (int q = 0; q < 4; ++q) {
-                        uint32_t o[32];
-                        tm_load32(to + 32 * q, o);
-                        tm_wait_load();
+                    for (int k = u; k < u + UNIT; ++k)
+                        mx = fmaxf(mx, __uint_as_float(s[q][k]));
+                    mx *= scale;
+                    const float ms = mx == -INFINITY ? 0.0f : mx;
 #pragma unroll
-                        for (int k = 0; k < 32; ++k)
-                            o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
-                        tm_store32(to + 32 * q, o);
+                    for (int k = u; k < u + UNIT; k += 2) {
+                        sum0 += ex2(fmaf(__uint_as_float(s[q][k]), scale, -ms));
+                        sum1 += ex2(fmaf(__uint_as_float(s[q][k + 1]), scale, -ms));
                     }
+                    unit_max[(32 * q + u) / UNIT] = mx;
+                    unit_sum[(32 * q + u) / UNIT] = sum0 + sum1;
+                    top = fmaxf(top, mx);
                 }
             }
-            const float ms = m == -INFINITY ? 0.0f : m * scale;
-            float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            if (page && live) {
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                uint32_t pk[32];
-#pragma unroll
-                for (int k = 0; k < 32; ++k) {
-                    const float a0 = ex2(fmaf(__uint_as_float(r[2 * q + (k >> 4)][2 * (k & 15)]), scale, -ms));
-                    const float a1 = ex2(fmaf(__uint_as_float(r[2 * q + (k >> 4)][2 * (k & 15) + 1]), scale, -ms));
-                    sum[k & 3] += a0 + a1;
-                    pk[k] = pack_sat(a0, a1);
-                }
-                tm_store32(ts + 32 * q, pk);
+                for (int u = 0; u < kTok / UNIT; ++u)
+                    if (u * UNIT < left)
+                        ls[t * (kTok / UNIT) + u] = unit_max[u] + __log2f(unit_sum[u]);
             }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-            tm_wait_store();
-            tm_fence_before();
-            bar_arrive(smem_addr(&sm.p_full[i]));
+            const float m1 = fmaxf(m, top), at = m1 == -INFINITY ? 0.0f : m1;
+            l *= ex2(m - at);
+#pragma unroll
+            for (int u = 0; u < kTok / UNIT; ++u)
+                l = fmaf(unit_sum[u], ex2(unit_max[u] - at), l);
+            m = m1;
         }
-        if (n > 0 && ok)
-            ok = __all_sync(0xffffffffu, bar_wait(smem_addr(&sm.s_full[i]), n & 1, failed));   // the last P V
-        tm_fence_after();
-        const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-        const int64_t part = (((int64_t)blockIdx.y * d.rows + row) * d.S + blockIdx.z);
-        const int64_t at = (int64_t)(first + tok) * (c.Hkv * c.g) + h * c.g + hh;
-#pragma unroll 1
-        for (int q = 0; q < 4; ++q) {
-            uint32_t o[32];
-            __syncwarp();
-            if (n > 0) {
-                tm_load32(to + 32 * q, o);
-                tm_wait_load();
-            } else {
-#pragma unroll
-                for (int k = 0; k < 32; ++k)
-                    o[k] = 0u;
-            }
-            if (row < rows) {
-                if (d.S == 1) {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        uint32_t w[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            w[e] = pack_sat(__uint_as_float(o[8 * k + 2 * e]) * inv, __uint_as_float(o[8 * k + 2 * e + 1]) * inv);
-                        *reinterpret_cast<uint4 *>(d.out + at * D + 32 * q + 8 * k) = make_uint4(w[0], w[1], w[2], w[3]);
-                    }
-                } else {
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        *reinterpret_cast<uint4 *>(d.o + part * D + 32 * q + 4 * k) =
-                            make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-                }
-            }
+        // two parts per split: the warpgroups' (with two M tiles one of them is empty)
+        if (live) {
+            float2 *ml = d.ml + (((int64_t)blockIdx.y * d.rows + (row - d.row0)) * d.S + blockIdx.z) * 2;
+            ml[two ? 0 : i] = make_float2(m, l);
+            if (two)
+                ml[1] = make_float2(-INFINITY, 0.0f);
         }
-        if (d.S > 1 && row < rows)
-            d.ml[part] = make_float2(m == -INFINITY ? m : m * scale, l);
     }
     tm_fence_before();
     __syncthreads();
@@ -511,92 +944,175 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(PagedArgs c, ChunkArg
     }
 }
 
-constexpr int kTcSmem = sizeof(TcSmem) + 1024;
-constexpr int kTcBlocks = 152;
+// --------------------------------------------------------------- launches ---
+
+constexpr int kTcSmem = sizeof(TcSmem) + 1024, kWeighSmem = sizeof(WeighSmem) + 1024;
 
 struct TcPlan {
-    int tiles, row_tiles, pairs, splits;      // pairs: staged and attended to per launch
+    int tiles, row_tiles, pairs, splits;      // pairs: staged and worked on per launch; row_tiles: of one launch
     int64_t pair_bytes;
 };
 
-TcPlan tc_plan(const PagedArgs &c, int max_new, int max_cached)
+// Splits of `blocks` blocks over `tiles` token tiles: the count with the
+// smallest waves x (fixed cost of a block, worth about 3 tiles, + its tiles).
+int tc_splits(int64_t blocks, int64_t tiles)
+{
+    int64_t best = INT64_MAX;
+    int splits = 1;
+    for (int64_t s = 1; s <= std::max<int64_t>(1, std::min(kPartBlocks / blocks, tiles)); ++s) {
+        const int64_t cost = (blocks * s + kTcBlocks - 1) / kTcBlocks * (3 + (tiles + s - 1) / s);
+        if (cost < best) {
+            best = cost;
+            splits = (int)s;
+        }
+    }
+    return splits;
+}
+
+int64_t row_tiles_of(const PagedArgs &c, int max_new) { return ((int64_t)max_new * c.g + kRows - 1) / kRows; }
+
+int weigh_unit(const PagedArgs &c) { return std::min(c.G, 32); }
+
+// page sums of one block of query rows of every pair
+int64_t sum_bytes(const PagedArgs &c, int64_t pairs)
+{
+    return pairs * kRows * ((int64_t)c.columns * c.G / weigh_unit(c)) * 4;
+}
+
+TcPlan tc_plan(const PagedArgs &c, int max_new, int max_cached, bool weights)
 {
     TcPlan p;
-    p.tiles = (int)(((int64_t)max_cached + max_new + kTok - 1) / kTok);
-    p.row_tiles = (int)(((int64_t)max_new * c.g + kRows - 1) / kRows);
+    // page tiles and fp16 tiles each end in one that may be part empty
+    p.tiles = (int)(((int64_t)max_cached + max_new + kTok - 1) / kTok + 1);
     p.pair_bytes = (int64_t)p.tiles * kTileBytes;
     p.pairs = (int)std::max<int64_t>(1, std::min<int64_t>(c.B * c.Hkv, kStageBytes / p.pair_bytes));
-    const int64_t blocks = (int64_t)p.pairs * p.row_tiles;
-    // one wave of blocks; a split has four tiles or more
-    p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(kTcBlocks / blocks, p.tiles / 4));
+    p.row_tiles = (int)row_tiles_of(c, max_new);
+    if (weights)
+        p.row_tiles = (int)std::max<int64_t>(1, std::min<int64_t>(p.row_tiles, kSumBytes / sum_bytes(c, p.pairs)));
+    p.splits = tc_splits((int64_t)p.pairs * p.row_tiles, p.tiles);
     return p;
 }
 
-template <class F>
-void launch_stage(const PagedArgs &c, const ChunkArgs &x, const StageArgs &a, dim3 grid, cudaStream_t s)
+// Workspace of a launch: staged tiles, the picked channels, results.
+size_t staged_bytes(const PagedArgs &c, const TcPlan &p)
 {
-    stage_kernel<F><<<grid, kStageThreads, 0, s>>>(c, x, a);
+    const int64_t all = (int64_t)c.B * c.Hkv;
+    return (size_t)std::min(all * p.pair_bytes, std::max(kStageBytes, p.pair_bytes)) + (size_t)(all * kChannels + 255) / 256 * 256;
+}
+
+cudaError_t stage(const PagedArgs &c, const ChunkArgs &x, const TcPlan &p, int pair0, int pairs, bool weights, void *ws,
+                  uint8_t *channels, cudaStream_t s, int *launches)
+{
+    if (!weights && !c.fmt) {
+        channels_kernel<<<pairs, kHeadDim, 0, s>>>(c, x, pair0, channels);
+        *launches += 1;
+    }
+    const StageArgs a{static_cast<uint8_t *>(ws), channels, p.tiles, pair0};
+    const dim3 grid(p.tiles, pairs);
+    *launches += 1;
+    if (c.fmt)
+        return launch_stage_fp8(c, x, a, weights, grid, s);
+    return c.bits == 2 ? launch_stage_2(c, x, a, weights, grid, s) : launch_stage_4(c, x, a, weights, grid, s);
+}
+
+TcArgs tc_args(const TcPlan &p, int pairs_at, void *ws, const uint8_t *channels)
+{
+    TcArgs d{};
+    d.tiles = static_cast<const uint8_t *>(ws);
+    d.channels = channels;
+    d.tiles_per_pair = p.tiles;
+    d.pair0 = pairs_at;
+    d.S = p.splits;
+    d.rows = p.row_tiles * kRows;
+    return d;
 }
 
 }  // namespace
 
-bool is_long_chunk(const PagedArgs &c, int max_new) { return (int64_t)max_new * c.g >= kLongRows; }
-
-size_t long_chunk_bytes(const PagedArgs &c, int max_new, int max_cached)
+// Both bounds only grow with max_new and max_cached.
+size_t long_attention_bytes(const PagedArgs &c, int max_new, int max_cached)
 {
-    if (!is_long_chunk(c, max_new))
-        return 0;
-    const TcPlan p = tc_plan(c, max_new, max_cached);
-    // staged tiles of one launch, and partial results: at most one wave of blocks has them
-    const int64_t staged = std::min<int64_t>((int64_t)c.B * c.Hkv * p.pair_bytes, std::max(kStageBytes, p.pair_bytes));
-    return (size_t)staged + (size_t)kTcBlocks * kRows * (kHeadDim + 2) * 4;
+    const TcPlan p = tc_plan(c, max_new, max_cached, false);
+    return staged_bytes(c, p) + (size_t)kPartBlocks * kRows * (kHeadDim + 2) * 4;
 }
 
-cudaError_t launch_long_chunk(const PagedArgs &c, const ChunkArgs &x, __half *out, void *ws, cudaStream_t s,
-                              int *launches)
+size_t long_weights_bytes(const PagedArgs &c, int max_new, int max_cached)
 {
-    const TcPlan p = tc_plan(c, x.max_new, x.max_cached);
+    const TcPlan p = tc_plan(c, max_new, max_cached, true);
+    const int64_t all = (int64_t)c.B * c.Hkv, one = sum_bytes(c, all), rows = row_tiles_of(c, max_new);
+    const int64_t sums = std::min(one * rows, std::max(kSumBytes, one));
+    return staged_bytes(c, p) + (size_t)sums + (size_t)(all * rows + kPartBlocks) * kRows * 16;
+}
+
+cudaError_t launch_long_attention(const PagedArgs &c, const ChunkArgs &x, __half *out, void *ws, cudaStream_t s,
+                                  int *launches)
+{
+    const TcPlan p = tc_plan(c, x.max_new, x.max_cached, false);
     const int all = c.B * c.Hkv;
-    TcOut d{};
-    d.tiles = static_cast<uint8_t *>(ws);
-    d.tiles_per_pair = p.tiles;
-    d.S = p.splits;
-    d.rows = p.row_tiles * kRows;
-    d.out = out;
-    d.o = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + p.pair_bytes * p.pairs);
-    d.ml = reinterpret_cast<float2 *>(d.o + (int64_t)p.pairs * d.rows * p.splits * kHeadDim);
-    const void *kernel = x.cap_log2 != 0.0f ? (const void *)tc_kernel<true> : (const void *)tc_kernel<false>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcSmem);
+    uint8_t *channels = static_cast<uint8_t *>(ws) + p.pair_bytes * p.pairs;
+    float *o = reinterpret_cast<float *>(channels + ((int64_t)p.pairs * kChannels + 255) / 256 * 256);
+    const bool cap = x.cap_log2 != 0.0f;
+    cudaError_t e = cudaFuncSetAttribute(cap ? (const void *)tc_kernel<true> : (const void *)tc_kernel<false>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kTcSmem);
     if (e != cudaSuccess)
         return e;
-    *launches = 0;
     for (int p0 = 0; p0 < all; p0 += p.pairs) {
         const int pairs = std::min(p.pairs, all - p0);
-        const StageArgs a{static_cast<uint8_t *>(ws), p.tiles, p0};
-        const dim3 grid(p.tiles, pairs);
-        if (c.fmt == KIVI_FP8_E4M3)
-            launch_stage<PageFmt<8, 0, KIVI_FP8_E4M3>>(c, x, a, grid, s);
-        else if (c.fmt == KIVI_FP8_E5M2)
-            launch_stage<PageFmt<8, 0, KIVI_FP8_E5M2>>(c, x, a, grid, s);
-        else if (c.bits == 2)
-            c.meta ? launch_stage<PageFmt<2, 1, 0>>(c, x, a, grid, s) : launch_stage<PageFmt<2, 0, 0>>(c, x, a, grid, s);
+        e = stage(c, x, p, p0, pairs, false, ws, channels, s, launches);
+        if (e != cudaSuccess)
+            return e;
+        TcArgs d = tc_args(p, p0, ws, channels);
+        d.out = out;
+        d.o = o;
+        d.ml = reinterpret_cast<float2 *>(o + (p.splits > 1 ? (int64_t)p.pairs * d.rows * p.splits * kHeadDim : 0));
+        const dim3 grid(p.row_tiles, pairs, p.splits);
+        if (cap)
+            tc_kernel<true><<<grid, kTcThreads, kTcSmem, s>>>(c, x, d);
         else
-            c.meta ? launch_stage<PageFmt<4, 1, 0>>(c, x, a, grid, s) : launch_stage<PageFmt<4, 0, 0>>(c, x, a, grid, s);
-        d.pair0 = p0;
-        const dim3 tgrid(p.row_tiles, pairs, p.splits);
-        if (x.cap_log2 != 0.0f)
-            tc_kernel<true><<<tgrid, kTcThreads, kTcSmem, s>>>(c, x, d);
-        else
-            tc_kernel<false><<<tgrid, kTcThreads, kTcSmem, s>>>(c, x, d);
-        *launches += 2;
-        if (p.splits > 1) {
+            tc_kernel<false><<<grid, kTcThreads, kTcSmem, s>>>(c, x, d);
+        *launches += 1;
+        e = cudaGetLastError();
+        if (e == cudaSuccess && p.splits > 1) {
             const float *ml = reinterpret_cast<const float *>(d.ml);
             e = launch_join(c, x, Parts{ml, ml + 1, d.o, 2, p.splits, p0, 0, d.rows}, out, pairs, s);
-            if (e != cudaSuccess)
-                return e;
             *launches += 1;
         }
-        e = cudaGetLastError();
+        if (e != cudaSuccess)
+            return e;
+    }
+    return cudaSuccess;
+}
+
+cudaError_t launch_long_weights(const PagedArgs &c, const ChunkArgs &x, float *weights, void *ws, cudaStream_t s,
+                                int *launches)
+{
+    const TcPlan p = tc_plan(c, x.max_new, x.max_cached, true);
+    const int all = c.B * c.Hkv, unit = weigh_unit(c);
+    float *ls = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + p.pair_bytes * p.pairs);
+    const bool cap = x.cap_log2 != 0.0f;
+    auto kernel = unit == 16 ? (cap ? tc_weigh_kernel<true, 16> : tc_weigh_kernel<false, 16>)
+                             : (cap ? tc_weigh_kernel<true, 32> : tc_weigh_kernel<false, 32>);
+    cudaError_t e = cudaFuncSetAttribute((const void *)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kWeighSmem);
+    if (e != cudaSuccess)
+        return e;
+    for (int p0 = 0; p0 < all; p0 += p.pairs) {
+        const int pairs = std::min(p.pairs, all - p0);
+        e = stage(c, x, p, p0, pairs, true, ws, nullptr, s, launches);
+        TcArgs d = tc_args(p, p0, ws, nullptr);
+        d.unit = unit;
+        d.units = (int)((int64_t)c.columns * c.G / unit);
+        d.ls = ls;
+        d.ml = reinterpret_cast<float2 *>(ls + ((int64_t)p.pairs * d.rows * d.units + 1) / 2 * 2);
+        const float *ml = reinterpret_cast<const float *>(d.ml);
+        for (int64_t r0 = 0; e == cudaSuccess && r0 < (int64_t)x.max_new * c.g; r0 += d.rows) {
+            d.row0 = (int)r0;
+            kernel<<<dim3(p.row_tiles, pairs, p.splits), kWeighThreads, kWeighSmem, s>>>(c, x, d);
+            e = cudaGetLastError();
+            if (e == cudaSuccess)
+                e = launch_weigh(c, x, Parts{ml, ml + 1, nullptr, 2, 2 * p.splits, p0, d.row0, d.rows}, ls, unit, d.units,
+                                 weights, pairs, s);
+            *launches += 2;
+        }
         if (e != cudaSuccess)
             return e;
     }

@@ -131,15 +131,17 @@ class Model:
 
     def attention(self, cap=0.0, causal=True, new=True, key_eps=HALF, tau=None):
         """Rows [N, Hq, D] and how far a kernel may be off each element.
-        Roundings: dequantised keys and values to fp16 (key_eps, HALF), the
-        probabilities to fp16 (HALF), the output to fp16 (HALF); fp32 sums
+        Roundings: dequantised keys to fp16 (key_eps), values to fp16, their
+        scale first (2 HALF), the probabilities to fp16 (HALF), the output to
+        fp16 (HALF); fp32 sums
         (2^-14 covers products and sums of a few thousand terms); the cap's
         tanh (cap 2^-21).  A score error d moves p_j by at most p_j (e^(2d) - 1).
         Below 2^-14 fp16 has a fixed step of 2^-24, half of which, 2^-25, is
         what a rounding is off there whatever the number's size: once for the
-        output, once for each value (times its p, which sum to 1), and once
-        for each 2^(s_j - m) it multiplies, the divisor being 1 or more: that
-        adds 2^-25 (2 + sum_j |v_j|) over the tokens a row sees.
+        output, twice for each value, which is carried halved (times its p,
+        which sum to 1), and once for each 2^(s_j - m) it multiplies, the
+        divisor being 1 or more: that adds 2^-25 (3 + sum_j |v_j|) over the
+        tokens a row sees.
         Few query rows: o = sum p s code - sum p s z, two fp32 sums of up to 64
         slices each (64 steps of 2^-24) whose terms are at most 4 max_c |v_jc|
         in size (a group's codes span its range, at most twice its largest
@@ -159,7 +161,7 @@ class Model:
                     sl = slice(self.off[b], self.off[b + 1])
                     out[sl, i] = o
                     seen = (p > 0).double()
-                    tol[sl, i] = (2.0 ** -16 * (p @ V.abs().amax(1, keepdim=True)) + 2.0 ** -25 * (2 + seen @ V.abs()) + HALF * o.abs() + (2 * HALF + 2.0 ** -14) * (p @ V.abs()) + dp @ V.abs() +
+                    tol[sl, i] = (2.0 ** -16 * (p @ V.abs().amax(1, keepdim=True)) + 2.0 ** -25 * (3 + seen @ V.abs()) + HALF * o.abs() + (3 * HALF + 2.0 ** -14) * (p @ V.abs()) + dp @ V.abs() +
                                   dp.sum(1, keepdim=True) * o.abs())
         return out, tol
 

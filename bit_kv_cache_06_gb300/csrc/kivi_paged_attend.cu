@@ -8,6 +8,7 @@
 // The parts of a row join as o = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i,
 // M = max_i m_i.
 #include <algorithm>
+#include <atomic>
 
 #include "kivi_paged_attend.cuh"
 #include "kivi_paged_decode.cuh"
@@ -131,20 +132,43 @@ int few_room(const PagedArgs &c, int max_new)
     return rows <= 4 ? 4 : (rows + 7) / 8 * 8;
 }
 
+// Blocks of a decode kernel that the current device holds at once; asked once
+// per device and kernel.
+cudaError_t resident_blocks(const PagedDecodeArgs &a, bool weights, int *blocks)
+{
+    static std::atomic<int> known[64][128];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return e;
+    const PagedArgs &c = a.c;
+    const int kind = c.fmt ? c.fmt - 1 : 2 + (c.bits == 4) * 2 + c.meta;             // 0 .. 5
+    const int kernel = ((kind * 4 + (c.G == 64 ? 1 : c.G == 128 ? 2 : 0)) * 2 + (a.rows > 4)) * 2 + weights;
+    std::atomic<int> *slot = dev < 64 ? &known[dev][kernel] : nullptr;
+    *blocks = slot ? slot->load(std::memory_order_relaxed) : 0;
+    if (*blocks > 0)
+        return cudaSuccess;
+    int sms = 0, per_sm = 0;
+    e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess)
+        e = paged_decode(a, weights, 0, nullptr, &per_sm);
+    if (e != cudaSuccess)
+        return e;
+    *blocks = std::max(per_sm, 1) * sms;
+    if (slot)
+        slot->store(*blocks, std::memory_order_relaxed);
+    return cudaSuccess;
+}
+
 // Splits of a decode launch: the count with the smallest waves x (fixed cost +
 // chunks per block) for the blocks the GPU holds at once -- the cost model of
 // kivi_decode_num_splits, for the longest sequence the bounds allow.
 cudaError_t few_splits(const PagedDecodeArgs &a, bool weights, int64_t blocks, int max_cached, int *splits)
 {
-    int dev = 0, sms = 0, per_sm = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess)
-        e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e == cudaSuccess)
-        e = paged_decode(a, weights, 0, nullptr, &per_sm);
+    int resident = 0;
+    const cudaError_t e = resident_blocks(a, weights, &resident);
     if (e != cudaSuccess)
         return e;
-    const int64_t resident = (int64_t)std::max(per_sm, 1) * sms;
     const int64_t chunks = std::max<int64_t>(1, ((int64_t)max_cached + kChunk - 1) / kChunk);
     const int64_t most = std::max<int64_t>(1, std::min<int64_t>(kDecodeBlocks / blocks, chunks));
     int64_t best = INT64_MAX;

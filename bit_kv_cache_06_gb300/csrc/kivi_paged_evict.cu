@@ -3,11 +3,18 @@
 // of its table row.  Nothing but page numbers and weights moves.
 //
 // One block per (sequence, kv head) pair.  The weights become 32-bit keys in
-// their order; four histogram passes of 8 bits find the key T of the last page
-// that stays and how many pages with exactly that key stay (the first ones,
-// from the lowest column).  One pass over the row in order then writes the kept
-// pages in place, to columns at or before the ones already read, and the
-// evicted ones to the workspace, from which they follow behind the kept ones.
+// their order, kept in shared memory (up to kCached of them; read again from
+// memory beyond that).  Three histogram passes of 11, 11 and 10 bits find the
+// key T of the last page that stays and how many pages with exactly that key stay
+// (the first ones, from the lowest column).  Each warp then owns a run of the
+// row: it counts the keys equal to T, then, knowing how many come before its
+// run, its kept pages, then writes its pages to their places in a copy of the
+// row; the copy goes back when every warp has read its part.
+//
+// Bound by latency: a row of 1000 pages is 4 KB, and the passes follow one
+// another.
+#include <algorithm>
+
 #include "kivi_paged.cuh"
 
 namespace kivi {
@@ -15,6 +22,10 @@ namespace {
 
 constexpr int kEvictThreads = 1024;
 constexpr int kWarps = kEvictThreads / 32;
+constexpr int kBins = 2048;
+constexpr int kCopies = 4;             // of the histogram: warps w, w + 4, ... share one
+constexpr int kAhead = 8;              // loads in flight per thread
+constexpr int kCached = 40960;         // keys in shared memory at most
 
 // Larger weights give larger keys; -0 counts as +0, NaN as the least.
 __device__ __forceinline__ unsigned order_key(float w)
@@ -25,7 +36,7 @@ __device__ __forceinline__ unsigned order_key(float w)
     return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
-// Sum of v over the threads before this one, and over the whole block.
+// Sums of v over the threads before this one, and over the whole block.
 __device__ __forceinline__ int2 block_scan(int v, int *warp_sums)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -50,76 +61,141 @@ __device__ __forceinline__ int2 block_scan(int v, int *warp_sums)
     return make_int2(before + incl - v, all);
 }
 
-__global__ void __launch_bounds__(kEvictThreads) evict_kernel(PagedArgs c, float *weights, int budget,
-                                                              int recent, int32_t *gone_ids)
+struct Moved {
+    int32_t id;
+    float weight;
+};
+
+__global__ void __launch_bounds__(kEvictThreads) evict_kernel(PagedArgs c, float *weights, int budget, int recent,
+                                                              Moved *copies, int cached)
 {
-    __shared__ int hist[256];
+    extern __shared__ unsigned smem[];
+    unsigned *keys = smem;                                   // [cached]
+    int *hist = reinterpret_cast<int *>(smem + cached);      // [kCopies][kBins]
     __shared__ int warp_sums[kWarps];
     __shared__ unsigned s_prefix;
     __shared__ int s_need;
-    const int p = blockIdx.x, b = p / c.Hkv, tid = threadIdx.x;
+    const int p = blockIdx.x, b = p / c.Hkv, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     PagedState st;
     const bool ok = paged_state(c, b, st);
     const int n = ok ? st.held : 0;
     if (!ok && tid == 0)
         atomicOr(c.control, KIVI_STATUS_BAD_STATE);
-    int32_t *row = c.table + (int64_t)p * c.columns;
-    float *w = weights + (int64_t)p * c.columns;
-    int32_t *gone = gone_ids + (int64_t)p * c.columns;
 
     if (n > budget) {
+        int32_t *row = c.table + (int64_t)p * c.columns;
+        float *w = weights + (int64_t)p * c.columns;
+        Moved *copy = copies + (int64_t)p * c.columns;
         const int fixed = min(recent, budget), cand = n - fixed;
+        const bool all_cached = n <= cached;
+        if (all_cached) {
+#pragma unroll 1
+            for (int i0 = tid; i0 < n; i0 += kAhead * kEvictThreads) {
+                float v[kAhead];
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k)
+                    v[k] = i0 + k * kEvictThreads < n ? w[i0 + k * kEvictThreads] : 0.0f;
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k)
+                    if (i0 + k * kEvictThreads < n)
+                        keys[i0 + k * kEvictThreads] = order_key(v[k]);
+            }
+        }
+        auto key = [&](int i) { return all_cached ? keys[i] : order_key(w[i]); };
+        __syncthreads();
         int need = budget - fixed;          // candidates that stay (fewer than cand)
-        // the key of the last one that stays, from its highest byte down
-        unsigned prefix = 0u;
-        for (int shift = 24; shift >= 0 && need > 0; shift -= 8) {
-            if (tid < 256)
-                hist[tid] = 0;
+        const bool none = need == 0;
+        unsigned prefix = 0u;               // key of the last one that stays, from its highest bits down
+        for (int pass = 0; pass < 3 && !none; ++pass) {
+            const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, above = pass == 0 ? 32 : pass == 1 ? 21 : 10;
+            const unsigned mask = pass == 2 ? 1023u : 2047u;
+            for (int i = tid; i < kCopies * kBins; i += kEvictThreads)
+                hist[i] = 0;
             __syncthreads();
+            int *mine = hist + (warp % kCopies) * kBins;
+#pragma unroll 4
             for (int i = tid; i < cand; i += kEvictThreads) {
-                const unsigned k = order_key(w[i]);
-                if (shift == 24 || (k ^ prefix) >> (shift + 8) == 0u)
-                    atomicAdd(&hist[(k >> shift) & 255u], 1);
+                const unsigned k = key(i);
+                if (pass == 0 || (k ^ prefix) >> above == 0u)
+                    atomicAdd(&mine[(k >> shift) & mask], 1);
             }
             __syncthreads();
-            if (tid == 0) {
-                int left = need, digit = 255;
-                while (digit > 0 && hist[digit] < left)
-                    left -= hist[digit--];
-                s_prefix = prefix | (unsigned)digit << shift;
-                s_need = left;
+            // from the largest digit down: the thread's two, and what lies above them
+            const int hi = kBins - 1 - 2 * tid, lo = hi - 1;
+            int count[2] = {0, 0};
+#pragma unroll
+            for (int k = 0; k < kCopies; ++k) {
+                count[0] += hist[k * kBins + hi];
+                count[1] += hist[k * kBins + lo];
+            }
+            int over = block_scan(count[0] + count[1], warp_sums).x;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                if (over < need && over + count[k] >= need) {
+                    s_prefix = prefix | (unsigned)(k ? lo : hi) << shift;
+                    s_need = need - over;
+                }
+                over += count[k];
             }
             __syncthreads();
             prefix = s_prefix;
             need = s_need;                  // of the keys with this prefix, this many stay
         }
-        const bool none = budget == fixed;  // no candidate stays
-        int kept0 = 0, gone0 = 0, equal0 = 0;
-        for (int i0 = 0; i0 < n; i0 += kEvictThreads) {
-            const int i = i0 + tid;
-            const bool in = i < n;
-            const int32_t id = in ? row[i] : 0;
-            const float wi = in ? w[i] : 0.0f;
-            const unsigned k = order_key(wi);
-            const bool candidate = i < cand;
-            const bool equal = candidate && !none && k == prefix;
-            const int2 eq = block_scan(equal, warp_sums);
-            const bool keep = in && (!candidate || (!none && (k > prefix || (equal && equal0 + eq.x < need))));
-            const int2 kp = block_scan(keep, warp_sums);   // its barriers: every thread has read row and w
-            if (keep) {
-                row[kept0 + kp.x] = id;
-                w[kept0 + kp.x] = wi;
-            } else if (in) {
-                gone[gone0 + tid - kp.x] = id;
+        // this warp's run of columns
+        const int per = (n + kWarps - 1) / kWarps, from = min(n, warp * per), to = min(n, from + per);
+        int equal = 0;                      // (counts are the same in every lane)
+        for (int i = from; i < to; i += 32)
+            equal += __popc(__ballot_sync(0xffffffffu, i + lane < min(to, cand) && !none && key(i + lane) == prefix));
+        const int equal0 = block_scan(lane == 0 ? equal : 0, warp_sums).x - (lane == 0 ? 0 : equal);
+        auto stays = [&](int i, int &seen) {    // column i (any lane's); seen: equal keys before this chunk
+            const bool in = i < to, candidate = i < cand;
+            const unsigned k = in ? key(i) : 0u;
+            const bool same = in && candidate && !none && k == prefix;
+            const unsigned votes = __ballot_sync(0xffffffffu, same);
+            const int rank = seen + __popc(votes & ((1u << lane) - 1u));
+            seen += __popc(votes);
+            return in && (!candidate || (!none && (k > prefix || (same && rank < need))));
+        };
+        int kept = 0, seen = equal0;
+        for (int i = from; i < to; i += 32)
+            kept += __popc(__ballot_sync(0xffffffffu, stays(i + lane, seen)));
+        int kept0 = block_scan(lane == 0 ? kept : 0, warp_sums).x - (lane == 0 ? 0 : kept);
+        int gone0 = budget + from - kept0;
+        seen = equal0;
+#pragma unroll 1
+        for (int i0 = from; i0 < to; i0 += 32 * kAhead) {
+            Moved m[kAhead];
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                const int i = i0 + 32 * k + lane;
+                m[k] = i < to ? Moved{row[i], w[i]} : Moved{0, 0.0f};
             }
-            equal0 += eq.y;
-            kept0 += kp.y;
-            gone0 += min(kEvictThreads, n - i0) - kp.y;
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                const int i = i0 + 32 * k;
+                const bool keep = stays(i + lane, seen);
+                const unsigned votes = __ballot_sync(0xffffffffu, keep), below = (1u << lane) - 1u;
+                if (i + lane < to) {
+                    const int at = keep ? kept0 + __popc(votes & below) : gone0 + __popc(~votes & below);
+                    copy[at] = Moved{m[k].id, keep ? m[k].weight : 0.0f};
+                }
+                kept0 += __popc(votes);
+                gone0 += max(0, min(32, to - i)) - __popc(votes);
+            }
         }
-        __syncthreads();
-        for (int i = tid; i < n - budget; i += kEvictThreads) {
-            row[budget + i] = gone[i];
-            w[budget + i] = 0.0f;
+        __syncthreads();                    // the row is read, the copy written
+#pragma unroll 1
+        for (int i0 = tid; i0 < n; i0 += kAhead * kEvictThreads) {
+            Moved m[kAhead];
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k)
+                m[k] = i0 + k * kEvictThreads < n ? copy[i0 + k * kEvictThreads] : Moved{0, 0.0f};
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k)
+                if (i0 + k * kEvictThreads < n) {
+                    row[i0 + k * kEvictThreads] = m[k].id;
+                    w[i0 + k * kEvictThreads] = m[k].weight;
+                }
         }
     }
     __threadfence();
@@ -136,12 +212,18 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(PagedArgs c, float
 
 }  // namespace
 
-size_t evict_bytes(const PagedArgs &c) { return (size_t)c.B * c.Hkv * c.columns * 4; }
+size_t evict_bytes(const PagedArgs &c) { return (size_t)c.B * c.Hkv * c.columns * sizeof(Moved); }
 
 cudaError_t launch_paged_evict(const PagedArgs &c, float *weights, int budget, int recent, void *ws,
                                cudaStream_t s, int *launches)
 {
-    evict_kernel<<<c.B * c.Hkv, kEvictThreads, 0, s>>>(c, weights, budget, recent, static_cast<int32_t *>(ws));
+    const int cached = std::min(c.columns, kCached);
+    const int smem = (cached + kCopies * kBins) * 4;
+    const cudaError_t e = cudaFuncSetAttribute(evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (kCached + kCopies * kBins) * 4);
+    if (e != cudaSuccess)
+        return e;
+    evict_kernel<<<c.B * c.Hkv, kEvictThreads, smem, s>>>(c, weights, budget, recent, static_cast<Moved *>(ws), cached);
     *launches = 1;
     return cudaGetLastError();
 }

@@ -72,7 +72,7 @@ class KiviPagedCache:
         if workspace.device != self.device or not workspace.is_contiguous():
             raise ValueError(f"workspace: contiguous on {self.device} is wanted")
         self.workspace = workspace
-        self._ws_bytes = workspace.numel() * workspace.element_size()
+        self._ws, self._ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
         self.control = torch.zeros(L.kivi_paged_control_bytes(ctypes.byref(self.params)) // 4,
                                    dtype=torch.int32, device=self.device)
         self.c = kivi.kivi_paged()
@@ -114,54 +114,62 @@ class KiviPagedCache:
         return self.c.kernel_launches
 
     # ---- calls ------------------------------------------------------------
-    def _stream(self, stream, tensors):
-        """The launch stream; tensors used on another one than their own are
-        kept from being handed out again before it is done with them."""
+    def _on(self, stream, tensors):
+        """The stream a call goes to, as the C ABI takes it; tensors that a
+        stream other than the current one uses are kept from being handed out
+        again before it is done with them."""
         current = torch.cuda.current_stream(self.device)
         if stream is None or stream == current:
-            return current
+            return current.cuda_stream
         if not torch.cuda.is_current_stream_capturing():
             for t in tensors:
                 if t is not None:
                     t.record_stream(stream)
-        return stream
+        return stream.cuda_stream
 
-    def _heads(self, name, x, heads, tokens=None):
-        d = self.shape.head_dim
-        if x.dtype != torch.float16 or x.dim() != 3 or x.shape[1] != heads or x.shape[2] != d or \
-                x.device != self.device or (tokens is not None and x.shape[0] != tokens):
+    def _call(self, name, *args):
+        """A launch, with this cache's device current."""
+        fn = getattr(kivi.load(), name)
+        if torch.cuda.current_device() == self.device.index:
+            _check(fn(self._c, *args), name)
+        else:
+            with torch.cuda.device(self.device):
+                _check(fn(self._c, *args), name)
+
+    def _heads(self, name, x, heads, tokens):
+        """Stride from token to token of x, fp16 [tokens, heads, d]."""
+        shape, d = x.shape, self.shape.head_dim
+        if len(shape) != 3 or shape[1] != heads or shape[2] != d or x.dtype != torch.float16 or \
+                x.device != self.device or (tokens is not None and shape[0] != tokens):
             raise ValueError(f"{name}: fp16 [{'tokens' if tokens is None else tokens}, {heads}, {d}] on "
-                             f"{self.device} is wanted; got {x.dtype} {list(x.shape)} on {x.device}")
-        if x.shape[0] > 0 and (x.stride(2) != 1 or (heads > 1 and x.stride(1) != d)):
-            raise ValueError(f"{name}: one token's heads have to lie side by side (strides {x.stride()})")
-        return x.stride(0) if x.shape[0] > 1 else max(heads * d, 8)
+                             f"{self.device} is wanted; got {x.dtype} {list(shape)} on {x.device}")
+        stride = x.stride()
+        if shape[0] > 0 and (stride[2] != 1 or (heads > 1 and stride[1] != d)):
+            raise ValueError(f"{name}: one token's heads have to lie side by side (strides {stride})")
+        return stride[0] if shape[0] > 1 else heads * d
 
     def _chunk(self, q, k, v, offsets, max_new, max_cached, softmax_scale, softcap, causal):
         s = self.shape
         if offsets is None or offsets.dtype != torch.int32 or offsets.numel() != s.batch + 1 or \
                 not offsets.is_contiguous() or offsets.device != self.device:
             raise ValueError(f"offsets: contiguous int32 [{s.batch + 1}] on {self.device} is wanted")
-        x = kivi.kivi_chunk()
-        n = None
+        n, q_ptr, k_ptr, v_ptr, q_stride, kv_stride = None, None, None, None, 0, 0
         if q is not None:
-            x.q, x.q_stride = q.data_ptr(), self._heads("q", q, s.num_q_heads)
+            q_ptr, q_stride = q.data_ptr(), self._heads("q", q, s.num_q_heads, None)
             n = q.shape[0]
         if k is not None:
-            x.k, x.kv_stride = k.data_ptr(), self._heads("k", k, s.num_kv_heads, n)
+            k_ptr, kv_stride = k.data_ptr(), self._heads("k", k, s.num_kv_heads, n)
             n = k.shape[0]
         if v is not None:
             if k is None:
                 raise ValueError("v without k")
-            x.v = v.data_ptr()
-            if self._heads("v", v, s.num_kv_heads, n) != x.kv_stride:
+            v_ptr = v.data_ptr()
+            if self._heads("v", v, s.num_kv_heads, n) != kv_stride:
                 raise ValueError("k and v have to have the same stride from token to token")
-        x.offsets = offsets.data_ptr()
-        x.num_tokens = n
-        x.max_new = n if max_new is None else int(max_new)
-        x.max_cached = self.max_cached if max_cached is None else int(max_cached)
-        x.softmax_scale, x.softcap = float(softmax_scale), float(softcap)
-        x.mask = kivi.KIVI_MASK_CAUSAL if causal else kivi.KIVI_MASK_FULL
-        return x
+        return ctypes.byref(kivi.kivi_chunk(
+            q_ptr, k_ptr, v_ptr, offsets.data_ptr(), q_stride, kv_stride, n,
+            n if max_new is None else max_new, self.max_cached if max_cached is None else max_cached,
+            softmax_scale, softcap, kivi.KIVI_MASK_CAUSAL if causal else kivi.KIVI_MASK_FULL, 0))
 
     def _pages(self, weights):
         want = (self.shape.batch * self.shape.num_kv_heads, self.columns)
@@ -176,10 +184,7 @@ class KiviPagedCache:
         [B + 1] on the device).  max_new bounds one sequence's count (default
         N).  n_tokens grows on the device."""
         x = self._chunk(None, k, v, offsets, max_new, 0, 0.0, 0.0, True)
-        with torch.cuda.device(self.device):
-            s = self._stream(stream, (k, v, offsets, self.control))
-            _check(kivi.load().kivi_paged_append(self._c, ctypes.byref(x), s.cuda_stream),
-                   "kivi_paged_append")
+        self._call("kivi_paged_append", x, self._on(stream, (k, v, offsets, self.control)))
 
     def attention(self, q, k=None, v=None, offsets=None, max_new=None, max_cached=None, softmax_scale=0.0,
                   softcap=0.0, causal=True, out=None, stream=None):
@@ -191,17 +196,17 @@ class KiviPagedCache:
         it is, the better the work is split.  Returns out, fp16
         [N, Hq, d]; rows outside every sequence stay as they are."""
         x = self._chunk(q, k, v, offsets, max_new, max_cached, softmax_scale, softcap, causal)
-        with torch.cuda.device(self.device):
-            s = self._stream(stream, (q, k, v, offsets, out, self.workspace))
-            if out is None:
-                with torch.cuda.stream(s):
-                    out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-            elif out.dtype != torch.float16 or out.shape != q.shape or not out.is_contiguous() or \
-                    out.device != self.device:
-                raise ValueError(f"out: contiguous fp16 {list(q.shape)} on {self.device} is wanted")
-            _check(kivi.load().kivi_paged_attention(self._c, ctypes.byref(x), out.data_ptr(),
-                                                    self.workspace.data_ptr(), self._ws_bytes,
-                                                    s.cuda_stream), "kivi_paged_attention")
+        if out is None:
+            if stream is None:
+                out = torch.empty(q.shape, dtype=torch.float16, device=self.device)
+            else:
+                with torch.cuda.stream(stream):
+                    out = torch.empty(q.shape, dtype=torch.float16, device=self.device)
+        elif out.dtype != torch.float16 or out.shape != q.shape or not out.is_contiguous() or \
+                out.device != self.device:
+            raise ValueError(f"out: contiguous fp16 {list(q.shape)} on {self.device} is wanted")
+        self._call("kivi_paged_attention", x, out.data_ptr(), self._ws, self._ws_bytes,
+                   self._on(stream, (q, k, v, offsets, out, self.workspace)))
         return out
 
     def weights(self, weights, q, k=None, offsets=None, max_new=None, max_cached=None, softmax_scale=0.0,
@@ -209,20 +214,13 @@ class KiviPagedCache:
         """Add to weights, fp32 [P, C], what each page gets of the softmax
         weights of `attention`'s queries."""
         x = self._chunk(q, k, None, offsets, max_new, max_cached, softmax_scale, softcap, causal)
-        ptr = self._pages(weights)
-        with torch.cuda.device(self.device):
-            s = self._stream(stream, (q, k, offsets, weights, self.workspace))
-            _check(kivi.load().kivi_paged_weights(self._c, ctypes.byref(x), ptr, self.workspace.data_ptr(),
-                                                  self._ws_bytes, s.cuda_stream), "kivi_paged_weights")
+        self._call("kivi_paged_weights", x, self._pages(weights), self._ws, self._ws_bytes,
+                   self._on(stream, (q, k, offsets, weights, self.workspace)))
         return weights
 
     def evict(self, weights, budget, recent=0, stream=None):
         """Every pair that holds more than `budget` pages keeps the `recent`
         newest ones and the heaviest others; table, weights and n_evicted
         follow (include/kivi.h, kivi_paged_evict)."""
-        ptr = self._pages(weights)
-        with torch.cuda.device(self.device):
-            s = self._stream(stream, (weights, self.workspace))
-            _check(kivi.load().kivi_paged_evict(self._c, ptr, int(budget), int(recent),
-                                                self.workspace.data_ptr(), self._ws_bytes,
-                                                s.cuda_stream), "kivi_paged_evict")
+        self._call("kivi_paged_evict", self._pages(weights), budget, recent, self._ws, self._ws_bytes,
+                   self._on(stream, (weights, self.workspace)))

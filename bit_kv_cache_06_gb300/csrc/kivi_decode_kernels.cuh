@@ -791,8 +791,14 @@ __global__ void __launch_bounds__(kThreads, 3)
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int r = lane >> 2, t = lane & 3;
-    const int split = blockIdx.x;
+    int split = blockIdx.x;
     const int p = blockIdx.y;
+    [[maybe_unused]] int tile = 0;    // paged: row tile; the tiles of a split run side by side and share its pages in L2
+    if constexpr (PG != 0) {
+        const int tiles = (arg.rows + GQ - 1) / GQ;
+        split = blockIdx.x / tiles;
+        tile = blockIdx.x - split * tiles;
+    }
     __shared__ int s_last;
     __shared__ int s_failed;          // a warp's bounded wait gave up
     [[maybe_unused]] DecodeArgs local;            // paged: with the state of this block's sequence
@@ -802,11 +808,11 @@ __global__ void __launch_bounds__(kThreads, 3)
         PagedState ps;
         int T;
         if (!sequence(arg.c, arg.x, p / arg.c.Hkv, first, T, ps)) {
-            if (tid == 0 && split == 0 && blockIdx.z == 0)
+            if (tid == 0 && split == 0 && tile == 0)
                 atomicOr(arg.c.control, KIVI_STATUS_BAD_STATE);
             return;
         }
-        prow0 = blockIdx.z * GQ;
+        prow0 = tile * GQ;
         row0 = arg.row0 + prow0;
         if (row0 >= T * arg.c.g)
             return;
@@ -871,7 +877,10 @@ __global__ void __launch_bounds__(kThreads, 3)
 
     // The history is read once: its copies may leave L2 first.
     uint64_t stream_policy;
-    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(stream_policy));
+    if (PG != 0 && paged_rows(arg) > GQ)
+        asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(stream_policy));
+    else
+        asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(stream_policy));
 
     // Fill stage i % STAGES with sub-slice i of this warp's run: one copy and
     // one barrier, issued by lane 0 when go is set (every lane computes the
@@ -2113,7 +2122,7 @@ cudaError_t launch_paged_mma(const PagedDecodeArgs &a, int pairs, cudaStream_t s
         return e;
     if (blocks_per_sm)
         return cudaOccupancyMaxActiveBlocksPerMultiprocessor(blocks_per_sm, kernel, kThreads, C::SMEM);
-    kernel<<<dim3((unsigned)a.d.S, (unsigned)pairs, (unsigned)((a.rows + GQ - 1) / GQ)), kThreads, C::SMEM, s>>>(a);
+    kernel<<<dim3((unsigned)(a.d.S * ((a.rows + GQ - 1) / GQ)), (unsigned)pairs), kThreads, C::SMEM, s>>>(a);
     return cudaGetLastError();
 }
 

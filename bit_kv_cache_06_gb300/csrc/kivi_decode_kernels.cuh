@@ -805,6 +805,7 @@ __global__ void __launch_bounds__(kThreads, 3)
     [[maybe_unused]] int prow0 = 0, row0 = 0;     // paged: first query row, in the chunk launch and in the pair
     [[maybe_unused]] int first = 0, cached16 = 0; // paged: first new token, fp16 tokens that are cached
     if constexpr (PG != 0) {
+        let_next_in();
         PagedState ps;
         int T;
         if (!sequence(arg.c, arg.x, p / arg.c.Hkv, first, T, ps)) {

@@ -99,6 +99,29 @@ __device__ __forceinline__ unsigned char *page_record(const PagedArgs &c, int p,
     return c.pool + (int64_t)id * c.rec_bytes;
 }
 
+// A kernel that reads what the one before it writes is launched as its
+// programmatic dependent: its blocks come in while the earlier ones run and
+// wait for the end of that grid and for its writes.  Every block of a dependent
+// waits, so a grid's end stands for the end of all before it.
+__device__ __forceinline__ void let_next_in() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+template <class... P, class... A>
+cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, unsigned block, size_t smem, cudaStream_t s, A... args)
+{
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
 cudaError_t launch_paged_append(const PagedArgs &c, const ChunkArgs &x, cudaStream_t s, int *launches);
 
 // Workspace bytes, which only grow with max_new and max_cached (both bounds of

@@ -23,10 +23,10 @@ __global__ void __launch_bounds__(128) join_kernel(PagedArgs c, ChunkArgs x, Par
     const int p = d.pair0 + blockIdx.y, b = p / c.Hkv, h = p % c.Hkv;
     int first, T;
     PagedState st;
-    if (!sequence(c, x, b, first, T, st))
-        return;
+    const bool some = sequence(c, x, b, first, T, st);
+    wait_for_previous();
     const int row = blockIdx.x * 4 + warp;
-    if (row >= T * c.g)
+    if (!some || row >= T * c.g)
         return;
     const int64_t at = (int64_t)(first + row / c.g) * (c.Hkv * c.g) + h * c.g + row % c.g;
     const int64_t part = ((int64_t)blockIdx.y * d.rows + row) * d.parts;
@@ -63,7 +63,10 @@ __global__ void __launch_bounds__(256) weigh_kernel(PagedArgs c, ChunkArgs x, Pa
     const int p = d.pair0 + blockIdx.y, b = p / c.Hkv, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int first, T;
     PagedState st;
-    if (!sequence(c, x, b, first, T, st))
+    const bool some = sequence(c, x, b, first, T, st);
+    let_next_in();
+    wait_for_previous();
+    if (!some)
         return;
     const int rows = min(d.rows, T * c.g - d.row0);
     const int col = blockIdx.x * 32 + lane;
@@ -225,15 +228,13 @@ size_t few_bytes(const PagedArgs &c, int max_new, bool weights)
 
 cudaError_t launch_join(const PagedArgs &c, const ChunkArgs &x, const Parts &d, __half *out, int pairs, cudaStream_t s)
 {
-    join_kernel<<<dim3((unsigned)(((int64_t)x.max_new * c.g + 3) / 4), pairs), 128, 0, s>>>(c, x, d, out);
-    return cudaGetLastError();
+    return launch_dependent(join_kernel, dim3((unsigned)(((int64_t)x.max_new * c.g + 3) / 4), pairs), 128, 0, s, c, x, d, out);
 }
 
 cudaError_t launch_weigh(const PagedArgs &c, const ChunkArgs &x, const Parts &d, const float *ls, int unit, int units,
                          float *weights, int pairs, cudaStream_t s)
 {
-    weigh_kernel<<<dim3((c.columns + 31) / 32, pairs), 256, 0, s>>>(c, x, d, ls, unit, units, weights);
-    return cudaGetLastError();
+    return launch_dependent(weigh_kernel, dim3((c.columns + 31) / 32, pairs), 256, 0, s, c, x, d, ls, unit, units, weights);
 }
 
 // The bounds below only grow with max_new and max_cached.

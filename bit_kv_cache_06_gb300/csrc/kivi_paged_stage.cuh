@@ -117,7 +117,10 @@ __global__ void __launch_bounds__(kStageThreads) stage_kernel(PagedArgs c, Chunk
     const int p = a.pair0 + blockIdx.y, b = p / c.Hkv, h = p % c.Hkv, tid = threadIdx.x;
     int first, T;
     PagedState st;
-    if (!sequence(c, x, b, first, T, st) || T == 0)
+    const bool some = sequence(c, x, b, first, T, st) && T > 0;
+    let_next_in();
+    wait_for_previous();
+    if (!some)
         return;
     const int deep = st.held * G, rowed = st.sink + st.window, shallow = rowed + (x.k ? T : 0);
     const int np = (deep + kTok - 1) / kTok, nf = (shallow + kTok - 1) / kTok;
@@ -355,10 +358,9 @@ cudaError_t launch_stage_of(const PagedArgs &c, const ChunkArgs &x, const StageA
                             cudaStream_t s)
 {
     using C = StageCfg<BITS, G, FMT>;
-    if (weights)
-        stage_kernel<C, true><<<grid, kStageThreads, 0, s>>>(c, x, a);
-    else
-        stage_kernel<C, false><<<grid, kStageThreads, 0, s>>>(c, x, a);
+    if (!weights)
+        return launch_dependent(stage_kernel<C, false>, grid, kStageThreads, 0, s, c, x, a);
+    stage_kernel<C, true><<<grid, kStageThreads, 0, s>>>(c, x, a);
     return cudaGetLastError();
 }
 

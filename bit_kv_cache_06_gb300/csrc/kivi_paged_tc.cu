@@ -459,6 +459,7 @@ __global__ void __launch_bounds__(256) prepare_kernel(PagedArgs c, ChunkArgs x, 
 {
     __shared__ float top[kHeadDim];
     __shared__ int scan[8];
+    let_next_in();
     if (blockIdx.x == 0)
         make_plan(c, x, pair0, jobs, row_tiles, blocks, plan, scan);
     else
@@ -508,6 +509,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(PagedArgs c, ChunkArg
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const Plan *plan = d.plan;
     const int block = blockIdx.x;
+    let_next_in();
+    wait_for_previous();
     if (block >= plan->blocks)
         return;
     const int64_t u0 = first_unit(plan, d.jobs, block), u1 = first_unit(plan, d.jobs, block + 1);
@@ -942,6 +945,7 @@ __global__ void __launch_bounds__(256) tc_join_kernel(PagedArgs c, ChunkArgs x, 
     __shared__ int count;
     __shared__ Job job;
     const Plan *plan = d.plan;
+    wait_for_previous();
     const int used = plan->blocks, first_block = blockIdx.x;
     if (first_block >= used - 1)
         return;
@@ -1021,6 +1025,8 @@ __global__ void __launch_bounds__(kWeighThreads, 1) tc_weigh_kernel(PagedArgs c,
     const bool some = job_of(c, x, d.pair0, blockIdx.y, d.row0, blockIdx.x, job, bad);
     if (bad && tid == 0 && blockIdx.x == 0 && blockIdx.z == 0)
         atomicOr(c.control, KIVI_STATUS_BAD_STATE);
+    let_next_in();
+    wait_for_previous();
     if (!some)
         return;
     const int t0 = (int)((int64_t)job.tiles * blockIdx.z / d.S), n = (int)((int64_t)job.tiles * (blockIdx.z + 1) / d.S) - t0;
@@ -1321,13 +1327,10 @@ cudaError_t launch_long_attention(const PagedArgs &c, const ChunkArgs &x, __half
         e = stage(c, x, p, p0, pairs, false, ws, channels, s);
         if (e != cudaSuccess)
             return e;
-        if (cap)
-            tc_kernel<true><<<blocks, kTcThreads, kTcSmem, s>>>(c, x, d);
-        else
-            tc_kernel<false><<<blocks, kTcThreads, kTcSmem, s>>>(c, x, d);
-        tc_join_kernel<<<dim3(blocks, kRows / kJoinRows), 256, 0, s>>>(c, x, d);
+        e = launch_dependent(cap ? tc_kernel<true> : tc_kernel<false>, dim3(blocks), kTcThreads, kTcSmem, s, c, x, d);
+        if (e == cudaSuccess)
+            e = launch_dependent(tc_join_kernel, dim3(blocks, kRows / kJoinRows), 256, 0, s, c, x, d);
         *launches += 4;
-        e = cudaGetLastError();
         if (e != cudaSuccess)
             return e;
     }
@@ -1358,8 +1361,7 @@ cudaError_t launch_long_weights(const PagedArgs &c, const ChunkArgs &x, float *w
         const float *ml = reinterpret_cast<const float *>(d.ml);
         for (int64_t r0 = 0; e == cudaSuccess && r0 < (int64_t)x.max_new * c.g; r0 += d.rows) {
             d.row0 = (int)r0;
-            kernel<<<dim3(p.row_tiles, pairs, p.splits), kWeighThreads, kWeighSmem, s>>>(c, x, d);
-            e = cudaGetLastError();
+            e = launch_dependent(kernel, dim3(p.row_tiles, pairs, p.splits), kWeighThreads, kWeighSmem, s, c, x, d);
             if (e == cudaSuccess)
                 e = launch_weigh(c, x, Parts{ml, ml + 1, nullptr, 2, 2 * p.splits, p0, d.row0, d.rows}, ls, unit, d.units,
                                  weights, pairs, s);

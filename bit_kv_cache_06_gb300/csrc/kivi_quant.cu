@@ -554,6 +554,7 @@ __global__ void __launch_bounds__(2 * G) paged_quantize_kernel(PagedArgs c, Chun
 {
     QuantArgs a;
     const int p = blockIdx.y;
+    let_next_in();
     unsigned char *rec = paged_append_record(c, x, blockIdx.x, p, a);
     if (rec)
         quantize_group<BITS, G, MF>(a, blockIdx.x, p, p / c.Hkv, p % c.Hkv, rec);
@@ -564,6 +565,7 @@ __global__ void __launch_bounds__(kThreads) paged_quantize_fp8_kernel(PagedArgs 
 {
     QuantArgs a;
     const int p = blockIdx.y;
+    let_next_in();
     unsigned char *rec = paged_append_record(c, x, blockIdx.x, p, a);
     if (rec)
         quantize_fp8_group<FMT>(a, blockIdx.x, p, p / c.Hkv, p % c.Hkv, rec);
@@ -582,6 +584,7 @@ __global__ void __launch_bounds__(kThreads) paged_rows_kernel(PagedArgs c, Chunk
     unsigned bad = 0;
     const int due = paged_quant_args(c, x, b, a, held, bad);
     int first = 0, T = 0;
+    wait_for_previous();                                      // the groups read rows that this kernel overwrites
     if (!bad) {
         chunk_of(x, b, first, T);
         const int take = (int)a.skip;
@@ -685,9 +688,9 @@ cudaError_t launch_paged_append(const PagedArgs &c, const ChunkArgs &x, cudaStre
     if (e != cudaSuccess)
         return e;
     const int rows = (int)std::min<int64_t>(x.max_new, (int64_t)c.Ns + c.R);
-    paged_rows_kernel<<<dim3((unsigned)((rows + kRowsPerPass - 1) / kRowsPerPass), (unsigned)pairs), kThreads, 0, s>>>(c, x);
     *launches = 2;
-    return cudaGetLastError();
+    return launch_dependent(paged_rows_kernel, dim3((unsigned)((rows + kRowsPerPass - 1) / kRowsPerPass), (unsigned)pairs),
+                            kThreads, 0, s, c, x);
 }
 
 cudaError_t launch_residual_copy(const ResidArgs &a, int pairs, cudaStream_t s)

@@ -1046,14 +1046,20 @@ __global__ void __launch_bounds__(kThreads, 3)
     [[maybe_unused]] auto cap_scores = [&](float (&sc)[2][2][NH], int kts) {
         if constexpr (PG != 0) {
             if (arg.x.cap_log2 != 0.0f) {
+                auto cap = [&](auto tanh_of) {
 #pragma unroll
-                for (int kt = 0; kt < 2; ++kt)
+                    for (int kt = 0; kt < 2; ++kt)
 #pragma unroll
-                    for (int rr = 0; rr < 2; ++rr)
+                        for (int rr = 0; rr < 2; ++rr)
 #pragma unroll
-                        for (int j = 0; j < NH; ++j)
-                            if (kt < kts)
-                                sc[kt][rr][j] = arg.x.cap_log2 * tanh_exp(sc[kt][rr][j] * arg.cap_log2_inv);
+                            for (int j = 0; j < NH; ++j)
+                                if (kt < kts)
+                                    sc[kt][rr][j] = arg.x.cap_log2 * tanh_of(sc[kt][rr][j] * arg.cap_log2_inv);
+                };
+                if (arg.x.cap_small)
+                    cap([](float y) { return tanh_far(y); });
+                else
+                    cap([](float y) { return tanh_any(y); });
             }
         }
     };

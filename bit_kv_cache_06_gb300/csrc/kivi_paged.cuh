@@ -31,6 +31,7 @@ struct ChunkArgs {
     int max_new, max_cached;          // bounds of one sequence's new and cached tokens
     float scale_log2;                 // softmax scale * log2(e)
     float cap_log2, cap_inv;          // cap * log2(e) and scale / cap; cap_log2 = 0: no cap
+    int cap_small;                    // cap below 64: an error of 2^-22 of it does not show
     int full;                         // every new token sees all of its sequence's
     int v8;                           // k, v rows and the fp16 rows 32-byte aligned
 };

@@ -85,6 +85,13 @@ PagedArgs paged_args(const kivi_paged *c)
     return a;
 }
 
+constexpr float kLog2e = 1.4426950408889634f;
+
+float softmax_scale(const kivi_paged *c, const kivi_chunk *x)
+{
+    return x->softmax_scale > 0.0f ? x->softmax_scale : 1.0f / std::sqrt((float)c->p.head_dim);
+}
+
 // What of a chunk a call reads.
 enum Uses { kUseQ = 1, kUseK = 2, kUseV = 4, kNewOptional = 8 };
 
@@ -94,6 +101,11 @@ int check_chunk(const kivi_paged *c, const kivi_chunk *x, int uses)
         x->max_cached < 0 || (x->mask != KIVI_MASK_CAUSAL && x->mask != KIVI_MASK_FULL) ||
         std::isnan(x->softmax_scale) || std::isnan(x->softcap) || std::isinf(x->softmax_scale) ||
         std::isinf(x->softcap))
+        return KIVI_ERR_INVALID_ARG;
+    // scale and cap in log2 units, and their quotient, are fp32 numbers
+    const float scale = softmax_scale(c, x);
+    if (!std::isfinite(scale * kLog2e) || (x->softcap > 0.0f && (!std::isfinite(x->softcap * kLog2e) ||
+                                                                 !std::isfinite(scale / x->softcap))))
         return KIVI_ERR_INVALID_ARG;
     if (x->num_tokens > INT_MAX / 2)
         return KIVI_ERR_UNSUPPORTED;
@@ -133,11 +145,14 @@ ChunkArgs chunk_args(const kivi_paged *c, const kivi_chunk *x)
     a.num_tokens = x->num_tokens;
     a.max_new = (int)std::min<int64_t>(x->max_new, x->num_tokens);
     a.max_cached = cached_bound(paged_args(&c->p), x->max_cached);
-    const float scale = x->softmax_scale > 0.0f ? x->softmax_scale : 1.0f / std::sqrt((float)c->p.head_dim);
-    a.scale_log2 = scale * 1.4426950408889634f;
-    if (x->softcap > 0.0f) {
-        a.cap_log2 = x->softcap * 1.4426950408889634f;
+    const float scale = softmax_scale(c, x);
+    a.scale_log2 = scale * kLog2e;
+    // a cap above 2^64 scale changes no score that fp32 holds to 24 bits: |q.k| < 2^52, y = scale q.k / cap < 2^-12,
+    // and tanh(y) = y (1 - y^2 / 3)
+    if (x->softcap > 0.0f && scale / x->softcap >= 0x1p-64f) {
+        a.cap_log2 = x->softcap * kLog2e;
         a.cap_inv = scale / x->softcap;
+        a.cap_small = x->softcap < 64.0f;
     }
     a.full = x->mask == KIVI_MASK_FULL;
     a.v8 = aligned(x->k, 32) && aligned(x->v, 32) && x->kv_stride % 16 == 0 && aligned(c->k_fp16, 32) &&

@@ -3,7 +3,7 @@
 // argument differ.
 #pragma once
 
-#include "kivi_paged.cuh"
+#include "kivi_paged_attend.cuh"
 
 namespace kivi {
 
@@ -41,14 +41,6 @@ __device__ __forceinline__ int paged_rows(const DecodeArgs &) { return 0; }
 __device__ __forceinline__ int paged_rows(const PagedDecodeArgs &arg) { return arg.rows; }
 __device__ __forceinline__ const __half *fresh_rows(const DecodeArgs &, int) { return nullptr; }
 __device__ __forceinline__ const __half *fresh_rows(const PagedDecodeArgs &arg, int value) { return value ? arg.x.v : arg.x.k; }
-
-// tanh(y) = 1 - 2 / (e^(2y) + 1): right to about 2^-23, absolutely.
-__device__ __forceinline__ float tanh_exp(float y)
-{
-    float e;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(y * 2.8853900817779268f));
-    return 1.0f - __fdividef(2.0f, e + 1.0f);
-}
 
 }  // namespace
 }  // namespace kivi

@@ -747,9 +747,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(PagedArgs c, ChunkArg
                 if constexpr (CAP) {
 #pragma unroll
                     for (int q = 0; q < 2; ++q)
-#pragma unroll
-                        for (int k = 0; k < 32; ++k)
-                            s[q][k] = __float_as_uint(score_log2(__uint_as_float(s[q][k]) * times, x));
+                        cap_scores(s[q], times, x);
                 }
                 const float scale = CAP ? 1.0f : x.scale_log2 * times;
                 const int left = (paged(j) ? deep - t * kTok : shallow - (t - np) * kTok) - 64 * half;
@@ -1132,11 +1130,8 @@ __global__ void __launch_bounds__(kWeighThreads, 1) tc_weigh_kernel(PagedArgs c,
             float top = -INFINITY;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                if constexpr (CAP) {
-#pragma unroll
-                    for (int k = 0; k < 32; ++k)
-                        s[q][k] = __float_as_uint(score_log2(__uint_as_float(s[q][k]) * times, x));
-                }
+                if constexpr (CAP)
+                    cap_scores(s[q], times, x);
                 if (left < 32 * q + 32) {
 #pragma unroll
                     for (int k = 0; k < 32; ++k)

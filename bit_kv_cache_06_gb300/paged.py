@@ -116,13 +116,15 @@ class KiviPagedCache:
     # ---- calls ------------------------------------------------------------
     def _on(self, stream, tensors):
         """The stream a call goes to, as the C ABI takes it; tensors that a
-        stream other than the current one uses are kept from being handed out
-        again before it is done with them."""
+        stream other than the current one uses, the cache's own among them, are
+        kept from being handed out again before it is done with them."""
         current = torch.cuda.current_stream(self.device)
         if stream is None or stream == current:
             return current.cuda_stream
         if not torch.cuda.is_current_stream_capturing():
-            for t in tensors:
+            own = (self.pool, self.k_fp16, self.v_fp16, self.table, self.n_tokens, self.n_evicted, self.control,
+                   self.workspace)
+            for t in tensors + own:
                 if t is not None:
                     t.record_stream(stream)
         return stream.cuda_stream
@@ -184,14 +186,15 @@ class KiviPagedCache:
         [B + 1] on the device).  max_new bounds one sequence's count (default
         N).  n_tokens grows on the device."""
         x = self._chunk(None, k, v, offsets, max_new, 0, 0.0, 0.0, True)
-        self._call("kivi_paged_append", x, self._on(stream, (k, v, offsets, self.control)))
+        self._call("kivi_paged_append", x, self._on(stream, (k, v, offsets)))
 
     def attention(self, q, k=None, v=None, offsets=None, max_new=None, max_cached=None, softmax_scale=0.0,
                   softcap=0.0, causal=True, out=None, stream=None):
         """Attention of new tokens q fp16 [N, Hq, d] over their sequence's
         cached tokens and over k, v fp16 [N, Hkv, d] of the new tokens
         themselves (causally, or all of them with causal=False; without k, v
-        over the cached tokens alone).  Appends nothing.  max_cached bounds
+        over the cached tokens alone).  Appends nothing.  max_new bounds the new
+        tokens of one sequence (default N: a batch of decode steps says 1), max_cached
         the cached tokens of any sequence (default: the cache's); the nearer
         it is, the better the work is split.  Returns out, fp16
         [N, Hq, d]; rows outside every sequence stay as they are."""
@@ -206,7 +209,7 @@ class KiviPagedCache:
                 out.device != self.device:
             raise ValueError(f"out: contiguous fp16 {list(q.shape)} on {self.device} is wanted")
         self._call("kivi_paged_attention", x, out.data_ptr(), self._ws, self._ws_bytes,
-                   self._on(stream, (q, k, v, offsets, out, self.workspace)))
+                   self._on(stream, (q, k, v, offsets, out)))
         return out
 
     def weights(self, weights, q, k=None, offsets=None, max_new=None, max_cached=None, softmax_scale=0.0,
@@ -215,7 +218,7 @@ class KiviPagedCache:
         weights of `attention`'s queries."""
         x = self._chunk(q, k, None, offsets, max_new, max_cached, softmax_scale, softcap, causal)
         self._call("kivi_paged_weights", x, self._pages(weights), self._ws, self._ws_bytes,
-                   self._on(stream, (q, k, offsets, weights, self.workspace)))
+                   self._on(stream, (q, k, offsets, weights)))
         return weights
 
     def evict(self, weights, budget, recent=0, stream=None):
@@ -223,4 +226,4 @@ class KiviPagedCache:
         newest ones and the heaviest others; table, weights and n_evicted
         follow (include/kivi.h, kivi_paged_evict)."""
         self._call("kivi_paged_evict", self._pages(weights), budget, recent, self._ws, self._ws_bytes,
-                   self._on(stream, (weights, self.workspace)))
+                   self._on(stream, (weights,)))

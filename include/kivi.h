@@ -450,7 +450,8 @@ typedef struct kivi_chunk {
                                  this; 0: as many as the table holds          */
     float softmax_scale;      /* <= 0: 1 / sqrt(d)                            */
     float softcap;            /* c > 0: scores become c tanh(score / c);
-                                 <= 0: as they are                            */
+                                 <= 0: as they are.  Both finite, and so are
+                                 scale log2 e, c log2 e and scale / c         */
     int32_t mask;             /* enum kivi_mask                               */
     int32_t reserved;         /* 0                                            */
 } kivi_chunk;

@@ -156,3 +156,14 @@ def test_binding_checks_its_tensors(L):
         c.weights(torch.zeros((4, 31)), q, kv, off)
     with pytest.raises(ValueError):
         c.evict(torch.zeros((4, 32), dtype=torch.float64), 3)
+
+
+def test_scales_and_caps_outside_fp32_are_refused(L):
+    _, c = cache(L)
+    cc, ws, n = ctypes.byref(c), 0x800000, 1 << 40
+    for kw in (dict(softmax_scale=3e38), dict(softcap=1e-40), dict(softcap=3e38), dict(softmax_scale=1e10, softcap=1e-30)):
+        x = ctypes.byref(chunk(**kw))
+        assert L.kivi_paged_attention(cc, x, 0x900000, ws, n, None) == kivi.KIVI_ERR_INVALID_ARG, kw
+        assert L.kivi_paged_weights(cc, x, 0xa00004, ws, n, None) == kivi.KIVI_ERR_INVALID_ARG, kw
+    assert L.kivi_paged_workspace_bytes(ctypes.byref(params()), 2 ** 31 - 1, 2 ** 31 - 1) > 0
+    assert c.kernel_launches == 0

@@ -182,6 +182,105 @@ def test_new_form_of_the_decode():
         assert ((ref.double().cpu() - want).abs().amax(-1) <= 2e-3 * want.abs().amax(-1)).all()
 
 
+def test_a_workspace_of_nan_patterns_changes_nothing():
+    """Nothing is read from the workspace that the call did not write there."""
+    for kw in (dict(), dict(bits=4, G=16, R=32), dict(bits=8, G=32, R=64, fp8=1)):
+        m = Model(3, 2, 4, seed=18, max_new=90, columns=40, **kw)
+        fill(m, [0, 333, 500])
+        assert m.gpu.status() == 0
+        for counts in ([1, 0, 1], [3, 16, 1], [90, 1, 0]):
+            m.chunk(counts)
+            m.gpu.workspace.fill_(0xff)
+            attend(m)
+            m.gpu.workspace.fill_(0xff)
+            w, x = torch.zeros((6, m.columns), device="cuda"), m.dev
+            m.gpu.weights(w, x["q"], x["k"], x["offsets"], x["max_new"])
+            close(w, *m.weights(), "weights")
+
+
+@pytest.mark.parametrize("cap", [1e4, 1e7, 1e25])
+def test_a_large_cap_keeps_the_scores(cap):
+    """Scores far below the cap: c tanh(s / c) is s (1 - (s/c)^2 / 3), which the
+    kernels hold to 2^-20 of the score, inside the bound's share of a score's
+    size without the cap's own term.  |s| < 100 here: p differs from the
+    uncapped one by less than 2 100^3 / 3e8 < 1 %, and the bound, which is
+    proportional to it, by as little."""
+    for counts in ([1], [9], [70]):
+        m = Model(1, 2, 4, seed=19, max_new=70, columns=24)
+        fill(m, [444])
+        m.chunk(counts)
+        x, n = m.dev, counts[0]
+        want, _ = m.attention(cap)
+        plain, tol = m.attention(0.0)
+        out = m.gpu.attention(x["q"], x["k"], x["v"], x["offsets"], n, softcap=cap)
+        close(out[:n], want, tol * 1.01, f"{counts}")
+        w = m.gpu.weights(torch.zeros((2, m.columns), device="cuda"), x["q"], x["k"], x["offsets"], n, softcap=cap)
+        close(w, m.weights(cap)[0], m.weights(0.0)[1] * 1.01, f"weights {counts}")
+
+
+def test_captured_long_chunks_share_a_workspace():
+    """Two caches, one workspace: a graph of each one's long chunk, replayed in
+    turn over growing caches; every replay sees its own."""
+    ms = [Model(2, 2, 4, seed=20 + i, max_new=80, columns=16, R=32) for i in range(2)]
+    ws = ms[0].gpu.workspace
+    caches = [paged.KiviPagedCache(m.gpu.shape, m.num_pages, 80, buffers=(
+        m.gpu.pool, m.gpu.k_fp16, m.gpu.v_fp16, m.gpu.table, m.gpu.n_tokens, m.gpu.n_evicted), workspace=ws) for m in ms]
+    runs, offsets = [], []                        # a graph reads its offsets again at every replay
+    side = torch.cuda.Stream()
+    for m, c in zip(ms, caches):
+        fill(m, [70, 5])
+        x = m.chunk([80, 21], pad=0)
+        q, k, v, off = x["q"].clone(), x["k"].clone(), x["v"].clone(), x["offsets"].clone()
+        out, w = torch.zeros_like(q), torch.zeros((4, m.columns), device="cuda")
+        g = torch.cuda.CUDAGraph()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side), torch.cuda.graph(g, stream=side):
+            c.attention(q, k, v, off, 80, out=out)
+            w.zero_()
+            c.weights(w, q, k, off, 80)
+        torch.cuda.current_stream().wait_stream(side)
+        runs.append((m, g, q, k, v, out, w))
+        offsets.append(off)
+    for i in range(3):
+        for m, g, q, k, v, out, w in runs:
+            x = m.chunk([80, 21], pad=0)
+            for t, name in ((q, "q"), (k, "k"), (v, "v")):
+                t.copy_(x[name])
+        for m, g, q, k, v, out, w in runs + runs:
+            g.replay()
+        for m, g, q, k, v, out, w in runs:
+            close(out, *m.attention(), f"replay {i}")
+            close(w, *m.weights(), f"weights {i}")
+            fill(m, [33, 40])
+
+
+def test_pairs_in_several_launches():
+    """A table so long that its tiles do not fit the workspace at once: the
+    pairs are staged and worked on in two launches."""
+    m = Model(4, 4, 1, seed=22, max_new=80, columns=4096)
+    fill(m, [300, 0, 77, 1])
+    m.chunk([80, 65, 1, 70])
+    n = m.gpu.kernel_launches
+    attend(m)
+    assert m.gpu.kernel_launches - n == 8
+    x = m.dev
+    w = m.gpu.weights(torch.zeros((16, m.columns), device="cuda"), x["q"], x["k"], x["offsets"], x["max_new"])
+    close(w, *m.weights(), "weights")
+
+
+def test_weights_of_many_rows_in_several_launches():
+    """Page sums of all query rows at once would be too large: eight tiles of
+    256 rows go in launches of fewer."""
+    m = Model(1, 1, 1, seed=23, max_new=2048, columns=40960)
+    fill(m, [200])
+    m.chunk([2048])
+    x = m.dev
+    n = m.gpu.kernel_launches
+    w = m.gpu.weights(torch.zeros((1, m.columns), device="cuda"), x["q"], x["k"], x["offsets"], 2048, max_cached=256)
+    assert m.gpu.kernel_launches - n > 3
+    close(w, *m.weights(), "weights")
+
+
 # ------------------------------------------------------------------- evict ---
 
 def random_weights(gen, P, C, kind):

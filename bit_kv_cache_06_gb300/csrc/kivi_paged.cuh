@@ -158,6 +158,7 @@ cudaError_t launch_weigh(const PagedArgs &c, const ChunkArgs &x, const Parts &d,
 
 // Many query rows (kivi_paged_tc.cu).
 size_t long_attention_bytes(const PagedArgs &c, int max_new, int max_cached);
+bool long_attention_fits(const PagedArgs &c, int max_new, int max_cached);
 size_t long_weights_bytes(const PagedArgs &c, int max_new, int max_cached);
 cudaError_t launch_long_attention(const PagedArgs &c, const ChunkArgs &x, __half *out, void *ws, cudaStream_t s,
                                   int *launches);

@@ -30,7 +30,7 @@ int check_paged_params(const kivi_params *p)
         return st;
     const int64_t pairs = (int64_t)p->batch * p->num_kv_heads;
     const int64_t columns = p->capacity_tokens / p->group;
-    if (columns < 1 || p->capacity_tokens + p->sink_tokens + p->residual > INT_MAX || columns * pairs > INT_MAX)
+    if (columns < 1 || p->capacity_tokens + p->sink_tokens + p->residual > INT_MAX - 4096 || columns * pairs > INT_MAX)
         return KIVI_ERR_UNSUPPORTED;
     return KIVI_OK;
 }
@@ -257,6 +257,8 @@ int kivi_paged_attention(kivi_paged *c, const kivi_chunk *x, void *out, void *wo
         return KIVI_ERR_INVALID_ARG;
     const ChunkArgs a = chunk_args(c, x);
     const PagedArgs pa = paged_args(c);
+    if (!long_attention_fits(pa, a.max_new, a.max_cached))
+        return KIVI_ERR_UNSUPPORTED;
     st = check_workspace(pa, a.max_new, x->max_cached, workspace, ws_bytes);
     if (st != KIVI_OK)
         return st;

@@ -44,21 +44,16 @@ __device__ __forceinline__ float tanh_any(float y)
 }
 
 // Scores in the log2 domain from products q.k times `times`: c log2(e)
-// tanh(tau q.k / c).  Small caps take the short form (x.cap_small): the long one
-// cost 3 % of a call of 8 new tokens (335 us against 325) and 9 % of the page
-// weights of 32.
-template <int N>
+// tanh(tau q.k / c).  Small caps (x.cap_small) take the short form: the long one
+// cost 9 % of the page weights of 32 tokens and 3 % of an attention of 8.
+template <bool SMALL, int N>
 __device__ __forceinline__ void cap_scores(uint32_t (&s)[N], float times, const ChunkArgs &x)
 {
     const float f = x.cap_inv * times;
-    if (x.cap_small) {
 #pragma unroll
-        for (int k = 0; k < N; ++k)
-            s[k] = __float_as_uint(x.cap_log2 * tanh_far(__uint_as_float(s[k]) * f));
-    } else {
-#pragma unroll
-        for (int k = 0; k < N; ++k)
-            s[k] = __float_as_uint(x.cap_log2 * tanh_any(__uint_as_float(s[k]) * f));
+    for (int k = 0; k < N; ++k) {
+        const float y = __uint_as_float(s[k]) * f;
+        s[k] = __float_as_uint(x.cap_log2 * (SMALL ? tanh_far(y) : tanh_any(y)));
     }
 }
 

@@ -14,8 +14,8 @@
 //   n = code - z       exact: (1024 + code) is the code's bits under an exponent,
 //                      and integers up to 2048 are fp16 numbers
 //   hi = n fp16(s/2)   one rounding (the scale's is another)
-// Runs whose zero point is beyond +-1000 (a narrow group far from zero) take
-// fp32 arithmetic instead.  What keys lose to rounding is multiplied by the
+// Runs whose zero point is beyond +-1000 (a narrow group far from zero), or whose
+// halved scale is not a normal fp16 number, take fp32 arithmetic instead.  What keys lose to rounding is multiplied by the
 // query, and a few channels of keys are far larger than the rest, so
 //   attention  the kChannels channels with the largest scales also get
 //              lo = (code - z) s/2 - hi, a tile of their own, 32-byte rows
@@ -34,6 +34,7 @@ namespace kivi {
 namespace {
 
 constexpr int kStageThreads = 256;
+constexpr float kLeastScale = 0x1p-14f;          // fp16's smallest normal number
 
 template <int BITS_, int G_, int FMT_>
 struct StageCfg {
@@ -211,7 +212,7 @@ __global__ void __launch_bounds__(kStageThreads) stage_kernel(PagedArgs c, Chunk
                 s[e] = 0.5f * scale_of(rec, mw, ch);
                 z[e] = scale_of(rec + mw * D, mw, ch);
             }
-            if (!(fabsf(z[0]) <= 1000.0f && fabsf(z[1]) <= 1000.0f))
+            if (!(fabsf(z[0]) <= 1000.0f && fabsf(z[1]) <= 1000.0f && fminf(s[0], s[1]) >= kLeastScale))
                 atomicOr(&s_kslow[k], 1u << (pair >> 3));
             kprm[k * 128 + pair] = bits_of(__floats2half2_rn(s[0], s[1]));
             kprm[k * 128 + 64 + pair] = bits_of(__floats2half2_rn(-1024.0f - z[0], -1024.0f - z[1]));
@@ -222,9 +223,10 @@ __global__ void __launch_bounds__(kStageThreads) stage_kernel(PagedArgs c, Chunk
                 const unsigned char *vs = raw_s + t / G * raw + head + u / C::SL * sub + 2 * C::SL * C::RB;
                 const int at = u % C::SL * C::VG + j;
                 const float z = scale_of(vs + C::SL * mw * C::VG, mw, at);
-                if (!(fabsf(z) <= 1000.0f))
+                const float s = 0.5f * scale_of(vs, mw, at);
+                if (!(fabsf(z) <= 1000.0f && s >= kLeastScale))
                     atomicOr(&s_vslow[t >> 5], 1u << (t & 31));
-                vprm[(2 * t) * C::VG + j] = __float2half_rn(0.5f * scale_of(vs, mw, at));
+                vprm[(2 * t) * C::VG + j] = __float2half_rn(s);
                 vprm[(2 * t + 1) * C::VG + j] = __float2half_rn(-1024.0f - z);
             }
         }

@@ -23,6 +23,7 @@
 //                   buffer of its own (four in turn), keys have a full low part,
 //                   and a thread turns its row's 128 scores into page sums.
 #include <algorithm>
+#include <climits>
 #include <type_traits>
 
 #include "kivi_paged_attend.cuh"
@@ -500,7 +501,8 @@ static_assert(kMTile * kHeadDim * 4 <= 2 * kImage, "join buffer");
 
 constexpr int kWorkers = kTcThreads - 32;        // all but the fetching warp: they meet between jobs
 
-template <bool CAP>
+// CAP: 0 no cap, 1 a small one, 2 any.
+template <int CAP>
 __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(PagedArgs c, ChunkArgs x, TcArgs d)
 {
     constexpr int D = kHeadDim;
@@ -744,12 +746,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(PagedArgs c, ChunkArg
                     tm_load32(ts + 64 * half + 32 * q, s[q]);
                 tm_wait_load();
                 const float times = paged(j) ? page_times : 1.0f;
-                if constexpr (CAP) {
+                if constexpr (CAP != 0) {
 #pragma unroll
                     for (int q = 0; q < 2; ++q)
-                        cap_scores(s[q], times, x);
+                        cap_scores<CAP == 1>(s[q], times, x);
                 }
-                const float scale = CAP ? 1.0f : x.scale_log2 * times;
+                const float scale = CAP != 0 ? 1.0f : x.scale_log2 * times;
                 const int left = (paged(j) ? deep - t * kTok : shallow - (t - np) * kTok) - 64 * half;
                 if (left < 64) {
 #pragma unroll
@@ -1012,7 +1014,7 @@ struct WeighSmem {
 
 // Step e is the scores of one M tile against one token tile (two M tiles: M tile
 // e & 1, tile e / 2; one: tile e), in S buffer e & 3, read by warpgroup e & 1.
-template <bool CAP, int UNIT>
+template <int CAP, int UNIT>
 __global__ void __launch_bounds__(kWeighThreads, 1) tc_weigh_kernel(PagedArgs c, ChunkArgs x, TcArgs d)
 {
     extern __shared__ uint8_t smem_raw[];
@@ -1117,7 +1119,7 @@ __global__ void __launch_bounds__(kWeighThreads, 1) tc_weigh_kernel(PagedArgs c,
                 break;
             tm_fence_after();
             const bool page = paged(j);
-            const float times = page ? page_times : 1.0f, scale = CAP ? 1.0f : x.scale_log2 * times;
+            const float times = page ? page_times : 1.0f, scale = CAP != 0 ? 1.0f : x.scale_log2 * times;
             const int left = page ? job.deep - t * kTok : shallow - (t - job.np) * kTok;
             float unit_max[kTok / UNIT], unit_sum[kTok / UNIT];
             uint32_t s[4][32];
@@ -1130,8 +1132,8 @@ __global__ void __launch_bounds__(kWeighThreads, 1) tc_weigh_kernel(PagedArgs c,
             float top = -INFINITY;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                if constexpr (CAP)
-                    cap_scores(s[q], times, x);
+                if constexpr (CAP != 0)
+                    cap_scores<CAP == 1>(s[q], times, x);
                 if (left < 32 * q + 32) {
 #pragma unroll
                     for (int k = 0; k < 32; ++k)
@@ -1282,6 +1284,13 @@ size_t long_attention_bytes(const PagedArgs &c, int max_new, int max_cached)
            (size_t)2 * kTcBlocks * kRows * (kHeadDim + 2) * 4;
 }
 
+// The plan counts in 32 bits.
+bool long_attention_fits(const PagedArgs &c, int max_new, int max_cached)
+{
+    const TcPlan p = tc_plan(c, max_new, max_cached, false);
+    return (int64_t)p.pairs * p.row_tiles <= INT_MAX / (kJobUnits + 2ll * p.tiles);
+}
+
 size_t long_weights_bytes(const PagedArgs &c, int max_new, int max_cached)
 {
     const TcPlan p = tc_plan(c, max_new, max_cached, true);
@@ -1298,14 +1307,13 @@ cudaError_t launch_long_attention(const PagedArgs &c, const ChunkArgs &x, __half
     uint8_t *channels = static_cast<uint8_t *>(ws) + p.pair_bytes * p.pairs;
     Plan *plan = reinterpret_cast<Plan *>(channels + channel_bytes(p.pairs));
     float *o = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(plan) + plan_bytes(most_jobs));
-    const bool cap = x.cap_log2 != 0.0f;
+    auto kernel = x.cap_log2 == 0.0f ? tc_kernel<0> : x.cap_small ? tc_kernel<1> : tc_kernel<2>;
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess)
         e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(cap ? (const void *)tc_kernel<true> : (const void *)tc_kernel<false>,
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize, kTcSmem);
+        e = cudaFuncSetAttribute((const void *)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcSmem);
     if (e != cudaSuccess)
         return e;
     const int blocks = std::min(sms, kTcBlocks);
@@ -1322,7 +1330,7 @@ cudaError_t launch_long_attention(const PagedArgs &c, const ChunkArgs &x, __half
         e = stage(c, x, p, p0, pairs, false, ws, channels, s);
         if (e != cudaSuccess)
             return e;
-        e = launch_dependent(cap ? tc_kernel<true> : tc_kernel<false>, dim3(blocks), kTcThreads, kTcSmem, s, c, x, d);
+        e = launch_dependent(kernel, dim3(blocks), kTcThreads, kTcSmem, s, c, x, d);
         if (e == cudaSuccess)
             e = launch_dependent(tc_join_kernel, dim3(blocks, kRows / kJoinRows), 256, 0, s, c, x, d);
         *launches += 4;
@@ -1338,9 +1346,9 @@ cudaError_t launch_long_weights(const PagedArgs &c, const ChunkArgs &x, float *w
     const TcPlan p = tc_plan(c, x.max_new, x.max_cached, true);
     const int all = c.B * c.Hkv, unit = weigh_unit(c);
     float *ls = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + p.pair_bytes * p.pairs);
-    const bool cap = x.cap_log2 != 0.0f;
-    auto kernel = unit == 16 ? (cap ? tc_weigh_kernel<true, 16> : tc_weigh_kernel<false, 16>)
-                             : (cap ? tc_weigh_kernel<true, 32> : tc_weigh_kernel<false, 32>);
+    const int cap = x.cap_log2 == 0.0f ? 0 : x.cap_small ? 1 : 2;
+    auto kernel = unit == 16 ? (cap == 0 ? tc_weigh_kernel<0, 16> : cap == 1 ? tc_weigh_kernel<1, 16> : tc_weigh_kernel<2, 16>)
+                             : (cap == 0 ? tc_weigh_kernel<0, 32> : cap == 1 ? tc_weigh_kernel<1, 32> : tc_weigh_kernel<2, 32>);
     cudaError_t e = cudaFuncSetAttribute((const void *)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kWeighSmem);
     if (e != cudaSuccess)
         return e;

@@ -433,7 +433,8 @@ enum kivi_mask {
 
 /* New tokens of a ragged batch.  Sequence b owns the tokens offsets[b] ..
  * offsets[b + 1] - 1 (none is legal); tokens outside every sequence are never
- * read or written.  Token i's query head h starts at q + (i q_stride + h d)
+ * read or written.  Unsupported: max_new Hq / Hkv above 2^22 - 64, and query
+ * rows of a pair times tokens they may see above about 2^45.  Token i's query head h starts at q + (i q_stride + h d)
  * halves, its kv head h at k + (i kv_stride + h d); the strides are multiples
  * of 8 and at least Hq d and Hkv d, so q, k and v may be slices of one
  * projection's output.  k and v may both be null (attention and weights):
@@ -458,7 +459,7 @@ typedef struct kivi_chunk {
 
 /* Table columns C and bytes of the control buffer; 0 if unsupported.  A paged
  * cache takes every kivi_params that kivi_params_validate accepts with
- * capacity_tokens + sink_tokens + residual below 2^31 and at least one column
+ * capacity_tokens + sink_tokens + residual below 2^31 - 4096 and at least one column
  * per pair, C P below 2^31.  Host only. */
 int32_t kivi_paged_columns(const kivi_params *p);
 size_t kivi_paged_control_bytes(const kivi_params *p);

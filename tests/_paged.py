@@ -41,10 +41,12 @@ class Model:
         self.outlier = torch.where(torch.rand((Hkv, D), generator=gen) < 0.02, 30.0, 1.0)
 
     # ---- inputs: q, k, v as slices of one buffer, with rows behind the last sequence
-    def chunk(self, counts, pad=3):
+    def chunk(self, counts, pad=3, scales=(1.0, 1.0, 1.0)):
         n, H = sum(counts), self.g * self.Hkv
         x = torch.randn((n + pad, H + 2 * self.Hkv, D), generator=self.gen)
         x[:, H:H + self.Hkv] *= self.outlier
+        for i, (lo, hi) in enumerate(((0, H), (H, H + self.Hkv), (H + self.Hkv, H + 2 * self.Hkv))):
+            x[:, lo:hi] *= scales[i]
         x[n:] = float("nan")                          # rows of no sequence
         qkv = x.half()
         self.counts = list(counts)

@@ -167,3 +167,16 @@ def test_scales_and_caps_outside_fp32_are_refused(L):
         assert L.kivi_paged_weights(cc, x, 0xa00004, ws, n, None) == kivi.KIVI_ERR_INVALID_ARG, kw
     assert L.kivi_paged_workspace_bytes(ctypes.byref(params()), 2 ** 31 - 1, 2 ** 31 - 1) > 0
     assert c.kernel_launches == 0
+
+
+def test_products_beyond_the_plan_are_unsupported(L):
+    p = params(batch=1, num_q_heads=4, num_kv_heads=1, capacity_tokens=1 << 30)
+    _, c = cache(L, p)
+    x = chunk(max_new=1 << 20, num_tokens=1 << 20, q_stride=512, kv_stride=128)
+    x.max_new = 65535 * 64 // 4
+    args = ctypes.byref(c), ctypes.byref(x), 0x900000, 0x800000
+    assert L.kivi_paged_attention(*args, 1000, None) == kivi.KIVI_ERR_UNSUPPORTED
+    x.max_cached = 1 << 20
+    assert L.kivi_paged_attention(*args, 1000, None) == kivi.KIVI_ERR_WORKSPACE
+    assert L.kivi_paged_columns(ctypes.byref(params(batch=1, num_kv_heads=1, num_q_heads=1, residual=32,
+                                                    capacity_tokens=(1 << 31) - 4096))) == 0

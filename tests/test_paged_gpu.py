@@ -218,6 +218,41 @@ def test_a_large_cap_keeps_the_scores(cap):
         close(w, m.weights(cap)[0], m.weights(0.0)[1] * 1.01, f"weights {counts}")
 
 
+@pytest.mark.parametrize("kw", [dict(bits=4, G=64, R=64), dict(bits=2, G=32, R=64), dict(bits=4, G=16, R=32, meta=1)])
+@pytest.mark.parametrize("counts,small", [([1, 1], -8), ([9, 2], -8), ([70, 33], -16)])
+def test_small_numbers(kw, counts, small):
+    """Keys near 2^-13 under queries near 2^12 and small values: scales below
+    fp16's normal numbers.  Beside the bound of `attention`: a key is carried
+    halved, so fp16's fixed step leaves 2^-24 of it, sum_c |q_c| tau 2^-24 of a
+    score; few query rows round p s to fp16, 2^-25 at least, which multiplies
+    |code - z| <= 2^bits - 1 (groups that span zero), per token seen and divided
+    by the sum of the p, which is one over the largest normalised p."""
+    m = Model(2, 2, 4, seed=25, max_new=70, columns=48, **kw)
+    scales = (2.0 ** 12, 2.0 ** -13, 2.0 ** small)
+    x = m.chunk([400, 333], scales=scales)
+    m.gpu.append(x["k"], x["v"], x["offsets"], x["max_new"])
+    m.append()
+    assert m.gpu.status() == 0
+    x = m.chunk(counts, scales=scales)
+    n = sum(counts)
+    out = m.gpu.attention(x["q"], x["k"], x["v"], x["offsets"], max(counts))
+    want, tol = m.attention()
+    step = torch.expm1(2 * 2.0 ** -24 * m.q[:n].double().abs().sum(-1, keepdim=True) / 128 ** 0.5)
+    for b in range(2):
+        sl = slice(m.off[b], m.off[b + 1])
+        for i in range(8):
+            K, V, cached, _ = m.keys(b, i // 4)
+            p, _ = m.softmax(b, i, K, cached, 0.0, True)
+            tol[sl, i] += 2 * step[sl, i] * V.abs().max()
+            if max(counts) * 4 <= 64:
+                tol[sl, i] += 2.0 ** -25 * (2 ** kw["bits"] - 1) * K.shape[0] * p.amax(1, keepdim=True)
+    close(out[:n], want, tol, "attention")
+    w = m.gpu.weights(torch.zeros((4, m.columns), device="cuda"), x["q"], x["k"], x["offsets"], max(counts))
+    # many rows carry halved keys here too: their low parts end at the same 2^-24
+    want, tol = m.weights()
+    close(w, want, tol + (float(step.max()) * want if max(counts) * 4 > 64 or kw["G"] == 16 else 0.0), "weights")
+
+
 def test_captured_long_chunks_share_a_workspace():
     """Two caches, one workspace: a graph of each one's long chunk, replayed in
     turn over growing caches; every replay sees its own."""

@@ -81,7 +81,7 @@ class KiviPagedCache:
                                  self.v_fp16.data_ptr(), self.table.data_ptr(),
                                  self.n_tokens.data_ptr(), self.n_evicted.data_ptr(),
                                  self.control.data_ptr()), "kivi_paged_init")
-        self._c = ctypes.byref(self.c)
+        self._c, self._lib, self._index = ctypes.byref(self.c), L, self.device.index
 
     @classmethod
     def from_cache(cls, cache, max_new=1, max_cached=0, workspace=None):
@@ -118,9 +118,10 @@ class KiviPagedCache:
         """The stream a call goes to, as the C ABI takes it; tensors that a
         stream other than the current one uses, the cache's own among them, are
         kept from being handed out again before it is done with them."""
-        current = torch.cuda.current_stream(self.device)
-        if stream is None or stream == current:
-            return current.cuda_stream
+        if stream is None:
+            return torch._C._cuda_getCurrentRawStream(self._index)
+        if stream == torch.cuda.current_stream(self.device):
+            return stream.cuda_stream
         if not torch.cuda.is_current_stream_capturing():
             own = (self.pool, self.k_fp16, self.v_fp16, self.table, self.n_tokens, self.n_evicted, self.control,
                    self.workspace)
@@ -131,17 +132,19 @@ class KiviPagedCache:
 
     def _call(self, name, *args):
         """A launch, with this cache's device current."""
-        fn = getattr(kivi.load(), name)
-        if torch.cuda.current_device() == self.device.index:
-            _check(fn(self._c, *args), name)
+        fn = getattr(self._lib, name)
+        if torch._C._cuda_getDevice() == self._index:
+            st = fn(self._c, *args)
         else:
             with torch.cuda.device(self.device):
-                _check(fn(self._c, *args), name)
+                st = fn(self._c, *args)
+        if st:
+            _check(st, name)
 
     def _heads(self, name, x, heads, tokens):
         """Stride from token to token of x, fp16 [tokens, heads, d]."""
         shape, d = x.shape, self.shape.head_dim
-        if len(shape) != 3 or shape[1] != heads or shape[2] != d or x.dtype != torch.float16 or \
+        if len(shape) != 3 or shape[1] != heads or shape[2] != d or x.dtype is not torch.float16 or \
                 x.device != self.device or (tokens is not None and shape[0] != tokens):
             raise ValueError(f"{name}: fp16 [{'tokens' if tokens is None else tokens}, {heads}, {d}] on "
                              f"{self.device} is wanted; got {x.dtype} {list(shape)} on {x.device}")
@@ -201,10 +204,10 @@ class KiviPagedCache:
         x = self._chunk(q, k, v, offsets, max_new, max_cached, softmax_scale, softcap, causal)
         if out is None:
             if stream is None:
-                out = torch.empty(q.shape, dtype=torch.float16, device=self.device)
+                out = q.new_empty(q.shape)
             else:
                 with torch.cuda.stream(stream):
-                    out = torch.empty(q.shape, dtype=torch.float16, device=self.device)
+                    out = q.new_empty(q.shape)
         elif out.dtype != torch.float16 or out.shape != q.shape or not out.is_contiguous() or \
                 out.device != self.device:
             raise ValueError(f"out: contiguous fp16 {list(q.shape)} on {self.device} is wanted")

@@ -2,7 +2,7 @@
 // a paged cache takes, and the joins of the parts.
 //
 //  query rows per pair      kernel
-//  up to kFewRows           decode kernel (kivi_decode_kernels.cuh), G >= 32
+//  up to most_few_rows()    decode kernel (kivi_decode_kernels.cuh), G >= 32
 //  more, or G = 16          tcgen05 kernels (kivi_paged_tc.cu)
 //
 // The parts of a row join as o = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i,
@@ -124,12 +124,30 @@ __global__ void __launch_bounds__(256) weigh_kernel(PagedArgs c, ChunkArgs x, Pa
 // ------------------------------------------------------------------- plans ---
 // Few query rows per pair: the decode kernel (kivi_paged_decode.cuh), which
 // streams the packed codes into the matrix instructions.  It takes 4 or 8 rows
-// and reads the pages again for the next 8.  Groups of 16 tokens it does not
-// know.
-constexpr int kFewRows = 64;
+// and reads the pages again for the next 8; the tcgen05 kernels dequantise them
+// once, for any number of rows.  Where the two meet (us, decode kernel against
+// tcgen05; 32 sequences of up to 8k tokens and 4-bit pages for attention, eight
+// of up to 32k and 2-bit pages for weights; FP8: 4 of 16k with 8 heads a kv
+// head, and eight of 32k):
+//                  8 rows     16         24         32         64         96
+//  attention, code                                  319 / 513  492 / 517  713 / 523
+//  attention, FP8  64 / 146   114 / 150  140 / 150  186 / 150
+//  weights, code                                    249 / 497  415 / 508  589 / 514
+//  weights, FP8    171 / 265  314 / 266
+// Groups of 16 tokens the decode kernel does not know.
+int most_few_rows(const PagedArgs &c, bool weights) { return !c.fmt ? 64 : weights ? 8 : 24; }
 constexpr int kDecodeBlocks = 4096;              // (pair, row tile, split) blocks of it that the workspace is sized for
 
-bool few_rows(const PagedArgs &c, int max_new) { return c.G >= 32 && (int64_t)max_new * c.g <= kFewRows; }
+bool few_rows(const PagedArgs &c, int max_new, bool weights)
+{
+    return c.G >= 32 && (int64_t)max_new * c.g <= most_few_rows(c, weights);
+}
+
+// the longest chunk of few rows, max_new at most
+int few_new(const PagedArgs &c, int max_new, bool weights)
+{
+    return std::min(max_new, std::max(1, most_few_rows(c, weights) / c.g));
+}
 
 cudaError_t paged_decode(const PagedDecodeArgs &a, bool weights, int pairs, cudaStream_t s, int *blocks_per_sm)
 {
@@ -265,24 +283,23 @@ cudaError_t launch_weigh(const PagedArgs &c, const ChunkArgs &x, const Parts &d,
 // The bounds below only grow with max_new and max_cached.
 size_t attention_bytes(const PagedArgs &c, int max_new, int max_cached)
 {
-    const int few = std::min(max_new, std::max(1, kFewRows / c.g));       // the longest chunk of few rows
-    const size_t bytes = few_bytes(c, few, false);
-    return few_rows(c, max_new) ? bytes : std::max(bytes, long_attention_bytes(c, max_new, max_cached));
+    const size_t bytes = few_bytes(c, few_new(c, max_new, false), false);
+    return few_rows(c, max_new, false) ? bytes : std::max(bytes, long_attention_bytes(c, max_new, max_cached));
 }
 
 size_t weights_bytes(const PagedArgs &c, int max_new, int max_cached)
 {
-    const int few = std::min(max_new, std::max(1, kFewRows / c.g));
+    const int few = few_new(c, max_new, true);
     const size_t sums = (size_t)c.B * c.Hkv * few_room(c, few) * ((size_t)c.columns * c.G / decode_unit(c)) * 4;
     const size_t bytes = few_bytes(c, few, true) + sums;
-    return few_rows(c, max_new) ? bytes : std::max(bytes, long_weights_bytes(c, max_new, max_cached));
+    return few_rows(c, max_new, true) ? bytes : std::max(bytes, long_weights_bytes(c, max_new, max_cached));
 }
 
 cudaError_t launch_paged_attention(const PagedArgs &c, const ChunkArgs &x, __half *out, void *ws, cudaStream_t s,
                                    int *launches)
 {
     *launches = 0;
-    if (!few_rows(c, x.max_new))
+    if (!few_rows(c, x.max_new, false))
         return launch_long_attention(c, x, out, ws, s, launches);
     const int pairs = c.B * c.Hkv;
     PagedDecodeArgs a = decode_args_of(c, x, few_room(c, x.max_new));
@@ -302,7 +319,7 @@ cudaError_t launch_paged_weights(const PagedArgs &c, const ChunkArgs &x, float *
                                  int *launches)
 {
     *launches = 0;
-    if (!few_rows(c, x.max_new))
+    if (!few_rows(c, x.max_new, true))
         return launch_long_weights(c, x, weights, ws, s, launches);
     const int pairs = c.B * c.Hkv, unit = decode_unit(c);
     PagedDecodeArgs a = decode_args_of(c, x, few_room(c, x.max_new));

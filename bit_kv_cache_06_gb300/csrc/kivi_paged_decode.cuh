@@ -1,6 +1,11 @@
 // kivi_paged_decode.cuh -- what the decode kernel needs to know of a paged
 // cache: its argument block, and the few places where the two kinds of
-// argument differ.
+// argument differ.  What it does and what bounds it (instruction issue) stands in
+// kivi_decode_kernels.cuh.  Measured over pages: eight sequences of up to 32768
+// tokens, 8 kv heads of 4 query heads, 2-bit: 60 us for 213 MB (3.5 TB/s; the
+// contiguous cache of 32768 tokens each: 59 us for 268 MB -- the longest
+// sequence's blocks set the time); 32 sequences of up to 8192 tokens, 32 query
+// rows in four passes, 4-bit: 322 us.
 #pragma once
 
 #include "kivi_paged_attend.cuh"

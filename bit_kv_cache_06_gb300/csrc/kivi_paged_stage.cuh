@@ -24,7 +24,9 @@
 // pairs of codes -- k and k + 8 (2-bit) or k + 4 (4-bit) -- and the values'
 // runs are those of the stored order; queries and outputs follow.
 //
-// Bound by memory: 96 to 256 bytes read and 512 (+32) written a token.
+// Bound by memory and latency: 96 to 256 bytes read and 512 (+32) written a token.
+// 8 pairs of 34816 tokens, 2-bit: 39 us, 152 MB written (most of it into L2), 3.9
+// TB/s.
 #pragma once
 
 #include "kivi_paged_attend.cuh"

@@ -21,6 +21,7 @@
 // are encoded between the two block barriers.  Traffic per token: 512 B
 // read and 64-128 B written.
 #include <algorithm>
+#include <type_traits>
 
 #include "kivi_paged.cuh"
 
@@ -244,12 +245,84 @@ __device__ __forceinline__ void store_value_codes(unsigned char *row, const uint
     }
 }
 
-// One key group of pair p = (b, h): tokens grp G .. grp G + G - 1 of the
-// concatenation, written as the record at `rec`.
-template <int BITS, int G, int MF>
-__device__ __forceinline__ void quantize_group(const QuantArgs &a, int64_t grp, int p, int b, int h,
-                                               unsigned char *rec)
+// Append to a paged cache: the same steps for a ragged batch whose state is on
+// the device.  Every block works out from n_tokens and the chunk's offsets what
+// its sequence flushes, quantises group blockIdx.x of it into the page the table
+// names, and leaves at once when there is no such group.  (One kernel with the
+// prefill's: as a function that both call, it cost the prefill 3 %.)  Bound by
+// memory: eight prompts of up to 8192 tokens, 8 kv heads, 2-bit: 56 us (4.7 TB/s,
+// the last wave part empty), and 6 us for the rows that stay fp16.
+
+// The concatenation [window, new tokens] of sequence b as QuantArgs, and the
+// groups its append flushes (0 when the sequence is skipped).
+__device__ __forceinline__ int paged_quant_args(const PagedArgs &c, const ChunkArgs &x, int b,
+                                                QuantArgs &a, int &held, unsigned &bad)
 {
+    int first, T;
+    PagedState st;
+    bad = chunk_of(x, b, first, T) ? 0u : KIVI_STATUS_BAD_STATE;
+    if (!bad && !paged_state(c, b, st))
+        bad = KIVI_STATUS_BAD_STATE;
+    if (!bad && (int64_t)st.n + T > 0x7fffffffll)
+        bad = KIVI_STATUS_BAD_STATE;
+    if (bad)
+        return 0;
+    const int due = flushed_groups(c, st.n + T) - st.flushed;
+    held = st.held;
+    if (held + due > c.columns) {
+        bad = KIVI_STATUS_CAPACITY;
+        return 0;
+    }
+    a.k_in = x.k + (int64_t)first * x.kv_stride;
+    a.v_in = x.v + (int64_t)first * x.kv_stride;
+    a.Hkv = c.Hkv;
+    a.in_sb = 0;
+    a.in_sh = kHeadDim;
+    a.in_st = x.kv_stride;
+    a.skip = min(T, c.Ns - st.sink);
+    a.k_res = c.k_fp16;
+    a.v_res = c.v_fp16;
+    a.rows = c.rows;
+    a.Ns = c.Ns;
+    a.R = c.R;
+    a.head = st.head;
+    a.n_old = st.window;
+    a.fp8_k_scale = c.fp8_k_scale;
+    a.fp8_v_scale = c.fp8_v_scale;
+    a.v8 = x.v8;
+    return due;
+}
+
+// Record of new group grp of pair p, or null when there is none to write.
+__device__ __forceinline__ unsigned char *paged_append_record(const PagedArgs &c, const ChunkArgs &x,
+                                                              int grp, int p, QuantArgs &a)
+{
+    int held = 0;
+    unsigned bad = 0;
+    const int due = paged_quant_args(c, x, p / c.Hkv, a, held, bad);
+    if (grp >= due)
+        return nullptr;
+    unsigned char *rec = page_record(c, p, held + grp);
+    if (!rec && threadIdx.x == 0)
+        atomicOr(c.control, KIVI_STATUS_BAD_PAGE);
+    return rec;
+}
+
+struct PagedQuantArgs {
+    PagedArgs c;
+    ChunkArgs x;
+};
+
+__device__ __forceinline__ const QuantArgs &quant_args(const QuantArgs &arg, const QuantArgs &) { return arg; }
+__device__ __forceinline__ const QuantArgs &quant_args(const PagedQuantArgs &, const QuantArgs &local) { return local; }
+
+// Key group blockIdx.x of pair blockIdx.y: tokens grp G .. grp G + G - 1 of the
+// concatenation, written as a record of the history or, for a paged cache
+// (PagedQuantArgs), into the page the table names.
+template <int BITS, int G, int MF, class Args>
+__global__ void __launch_bounds__(2 * G) quantize_kv_kernel(Args arg)
+{
+    constexpr bool PAGED = std::is_same<Args, PagedQuantArgs>::value;
     constexpr int D = kHeadDim;
     constexpr int W = G / 16;          // warps
     constexpr int NT = 32 * W;         // threads
@@ -269,6 +342,19 @@ __device__ __forceinline__ void quantize_group(const QuantArgs &a, int64_t grp, 
 
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     const int q = lane >> 3, c16 = lane & 7;
+    [[maybe_unused]] QuantArgs local;
+    [[maybe_unused]] unsigned char *page = nullptr;
+    if constexpr (PAGED) {
+        let_next_in();
+        page = paged_append_record(arg.c, arg.x, blockIdx.x, blockIdx.y, local);
+        if (!page)
+            return;
+    }
+    const QuantArgs &a = quant_args(arg, local);
+    const int64_t grp = blockIdx.x;
+    const int p = blockIdx.y;
+    const int b = p / a.Hkv;
+    const int h = p % a.Hkv;
     const int t0 = 16 * w + q;                      // the lane's rows: t0 + 4 i
     const int64_t u0 = grp * G + t0;
 
@@ -287,6 +373,12 @@ __device__ __forceinline__ void quantize_group(const QuantArgs &a, int64_t grp, 
             load_row16<false>(concat_row(a, a.v_res, a.v_in, p, b, h, u0 + 4 * i) + 16 * c16, vx[i]);
         }
     }
+    unsigned char *rec;
+    if constexpr (PAGED)
+        rec = page;
+    else
+        rec = a.hist + ((int64_t)p * (a.cap / G) + a.n_quant / G + grp) * RC::BYTES;
+
     // ---- keys: per-channel min/max over the G tokens (fp16, exact) --------
     {
         uint32_t mm[16];
@@ -398,16 +490,6 @@ __device__ __forceinline__ void quantize_group(const QuantArgs &a, int64_t grp, 
     }
 }
 
-template <int BITS, int G, int MF>
-__global__ void __launch_bounds__(2 * G) quantize_kv_kernel(QuantArgs a)
-{
-    const int64_t grp = blockIdx.x;
-    const int p = blockIdx.y;
-    unsigned char *rec =
-        a.hist + ((int64_t)p * (a.cap / G) + a.n_quant / G + grp) * Rec<BITS, G, MF>::BYTES;
-    quantize_group<BITS, G, MF>(a, grp, p, p / a.Hkv, p % a.Hkv, rec);
-}
-
 // ----------------------------------------------------------------- FP8 KV ---
 // "09 -- KV Cache Quantization", "The lazy default: FP8 KV"; "4.4 KV Cache
 // quantization", section 4.2: every element becomes fp8(x / scale) -- x / scale
@@ -490,76 +572,6 @@ __global__ void __launch_bounds__(kThreads) residual_copy_kernel(ResidArgs a)
 }
 
 // ------------------------------------------------------------ paged append ---
-// The same two steps for a ragged batch whose state is on the device: every
-// block works out from n_tokens and the chunk's offsets what its sequence
-// flushes, quantises group blockIdx.x of it into the page the table names, and
-// leaves at once when there is no such group.
-
-// The concatenation [window, new tokens] of sequence b as QuantArgs, and the
-// groups its append flushes (0 when the sequence is skipped).
-__device__ __forceinline__ int paged_quant_args(const PagedArgs &c, const ChunkArgs &x, int b,
-                                                QuantArgs &a, int &held, unsigned &bad)
-{
-    int first, T;
-    PagedState st;
-    bad = chunk_of(x, b, first, T) ? 0u : KIVI_STATUS_BAD_STATE;
-    if (!bad && !paged_state(c, b, st))
-        bad = KIVI_STATUS_BAD_STATE;
-    if (!bad && (int64_t)st.n + T > 0x7fffffffll)
-        bad = KIVI_STATUS_BAD_STATE;
-    if (bad)
-        return 0;
-    const int due = flushed_groups(c, st.n + T) - st.flushed;
-    held = st.held;
-    if (held + due > c.columns) {
-        bad = KIVI_STATUS_CAPACITY;
-        return 0;
-    }
-    a.k_in = x.k + (int64_t)first * x.kv_stride;
-    a.v_in = x.v + (int64_t)first * x.kv_stride;
-    a.in_sb = 0;
-    a.in_sh = kHeadDim;
-    a.in_st = x.kv_stride;
-    a.skip = min(T, c.Ns - st.sink);
-    a.k_res = c.k_fp16;
-    a.v_res = c.v_fp16;
-    a.rows = c.rows;
-    a.Ns = c.Ns;
-    a.R = c.R;
-    a.head = st.head;
-    a.n_old = st.window;
-    a.fp8_k_scale = c.fp8_k_scale;
-    a.fp8_v_scale = c.fp8_v_scale;
-    a.v8 = x.v8;
-    return due;
-}
-
-// Record of new group grp of pair p, or null when there is none to write.
-__device__ __forceinline__ unsigned char *paged_append_record(const PagedArgs &c, const ChunkArgs &x,
-                                                              int grp, int p, QuantArgs &a)
-{
-    int held = 0;
-    unsigned bad = 0;
-    const int due = paged_quant_args(c, x, p / c.Hkv, a, held, bad);
-    if (grp >= due)
-        return nullptr;
-    unsigned char *rec = page_record(c, p, held + grp);
-    if (!rec && threadIdx.x == 0)
-        atomicOr(c.control, KIVI_STATUS_BAD_PAGE);
-    return rec;
-}
-
-template <int BITS, int G, int MF>
-__global__ void __launch_bounds__(2 * G) paged_quantize_kernel(PagedArgs c, ChunkArgs x)
-{
-    QuantArgs a;
-    const int p = blockIdx.y;
-    let_next_in();
-    unsigned char *rec = paged_append_record(c, x, blockIdx.x, p, a);
-    if (rec)
-        quantize_group<BITS, G, MF>(a, blockIdx.x, p, p / c.Hkv, p % c.Hkv, rec);
-}
-
 template <int FMT>
 __global__ void __launch_bounds__(kThreads) paged_quantize_fp8_kernel(PagedArgs c, ChunkArgs x)
 {
@@ -627,10 +639,10 @@ cudaError_t launch_quantize_bits(int G, const QuantArgs &a, int pairs, cudaStrea
 {
     dim3 grid((unsigned)(a.nq_new / G), (unsigned)pairs);
     switch (G) {
-    case 16: quantize_kv_kernel<BITS, 16, MF><<<grid, 32, 0, s>>>(a); break;
-    case 32: quantize_kv_kernel<BITS, 32, MF><<<grid, 64, 0, s>>>(a); break;
-    case 64: quantize_kv_kernel<BITS, 64, MF><<<grid, 128, 0, s>>>(a); break;
-    case 128: quantize_kv_kernel<BITS, 128, MF><<<grid, 256, 0, s>>>(a); break;
+    case 16: quantize_kv_kernel<BITS, 16, MF, QuantArgs><<<grid, 32, 0, s>>>(a); break;
+    case 32: quantize_kv_kernel<BITS, 32, MF, QuantArgs><<<grid, 64, 0, s>>>(a); break;
+    case 64: quantize_kv_kernel<BITS, 64, MF, QuantArgs><<<grid, 128, 0, s>>>(a); break;
+    case 128: quantize_kv_kernel<BITS, 128, MF, QuantArgs><<<grid, 256, 0, s>>>(a); break;
     default: return cudaErrorInvalidValue;
     }
     return cudaGetLastError();
@@ -662,11 +674,12 @@ cudaError_t launch_quantize_fp8(int fmt, const QuantArgs &a, int pairs, cudaStre
 template <int BITS, int MF>
 static void launch_paged_quantize(const PagedArgs &c, const ChunkArgs &x, dim3 grid, cudaStream_t s)
 {
+    const PagedQuantArgs a{c, x};
     switch (c.G) {
-    case 16: paged_quantize_kernel<BITS, 16, MF><<<grid, 32, 0, s>>>(c, x); break;
-    case 32: paged_quantize_kernel<BITS, 32, MF><<<grid, 64, 0, s>>>(c, x); break;
-    case 64: paged_quantize_kernel<BITS, 64, MF><<<grid, 128, 0, s>>>(c, x); break;
-    default: paged_quantize_kernel<BITS, 128, MF><<<grid, 256, 0, s>>>(c, x); break;
+    case 16: quantize_kv_kernel<BITS, 16, MF, PagedQuantArgs><<<grid, 32, 0, s>>>(a); break;
+    case 32: quantize_kv_kernel<BITS, 32, MF, PagedQuantArgs><<<grid, 64, 0, s>>>(a); break;
+    case 64: quantize_kv_kernel<BITS, 64, MF, PagedQuantArgs><<<grid, 128, 0, s>>>(a); break;
+    default: quantize_kv_kernel<BITS, 128, MF, PagedQuantArgs><<<grid, 256, 0, s>>>(a); break;
     }
 }
 

@@ -454,6 +454,31 @@ def test_other_streams_and_equal_bits():
     assert torch.equal(a[:47], b[:47]) and torch.equal(wa, wb)
 
 
+def test_two_caches_on_two_streams_at_once():
+    """Calls of two caches with workspaces of their own, enqueued in turn on two
+    streams without waiting, give the bits they give one after the other."""
+    ms = [Model(2, 2, 4, seed=30 + i, max_new=80, columns=24) for i in range(2)]
+    streams = [torch.cuda.Stream() for _ in ms]
+    for m in ms:
+        fill(m, [333, 500])
+    for counts in ([80, 33], [1, 1], [7, 3]):
+        xs = [m.chunk(counts, pad=0) for m in ms]
+        refs = []
+        for m, x in zip(ms, xs):
+            w = m.gpu.weights(torch.zeros((4, m.columns), device="cuda"), x["q"], x["k"], x["offsets"], x["max_new"])
+            refs.append((m.gpu.attention(x["q"], x["k"], x["v"], x["offsets"], x["max_new"]), w))
+        outs = [[torch.zeros_like(a) for _ in range(8)] for a, _ in refs]
+        ws = [[torch.zeros_like(w) for _ in range(8)] for _, w in refs]
+        torch.cuda.synchronize()
+        for i in range(8):
+            for j, (m, x, s) in enumerate(zip(ms, xs, streams)):
+                m.gpu.attention(x["q"], x["k"], x["v"], x["offsets"], x["max_new"], out=outs[j][i], stream=s)
+                m.gpu.weights(ws[j][i], x["q"], x["k"], x["offsets"], x["max_new"], stream=s)
+        torch.cuda.synchronize()
+        for j, (a, w) in enumerate(refs):
+            assert all(torch.equal(o, a) for o in outs[j]) and all(torch.equal(o, w) for o in ws[j])
+
+
 def test_pool_offsets_pass_32_bits():
     """Pages beyond the first 4 GB of a pool, written and read."""
     m = Model(1, 2, 2, seed=12)
